@@ -18,7 +18,8 @@ from ._lib import (EXPORTS, HSAError, hsa_block_sums, hsa_decode_step,  # noqa: 
                    hsa_prefill_host,
                    hsa_prefill_host_workspace_size,
                    hsa_decode_workspace_size, hsa_index, hsa_index_workspace_size, hsa_params,
-                   hsa_select_blocks, hsa_select_tokens, hsa_sparse_attn, kernel_launches, lib_path, load,
+                   hsa_qk_norm_rope, hsa_select_blocks, hsa_select_tokens, hsa_sparse_attn, hsa_tree_commit,
+                   hsa_tree_plan, hsa_tree_step, hsa_tree_workspace_size, kernel_launches, lib_path, load,
                    params, status_string)
 from .build import build  # noqa: F401
 
@@ -55,3 +56,38 @@ def sparse_attn(Q, K, V, indices, scale: float = 0.0, stream=None):
     O = torch.empty_like(Q)
     hsa_sparse_attn(p, Lq, K.shape[0], Q, K, V, indices, O, stream)
     return O
+
+
+def qk_norm_rope(Q, K, q_weight=None, k_weight=None, inv_freq=None, positions=None, pos0: int = 0,
+                 eps: float = 1e-6, interleaved: bool = False, stream=None):
+    """(Q [L][H][d], K [L][d]) bf16: each head RMS-normed and its first 2 * len(inv_freq) values rotated.
+
+    Q and K may be rows of a wider projection (only a token's own values must be
+    contiguous); either may be None. Row i is at positions[i] (int32) or pos0 + i.
+    Rows with a negative position come back as zeros.
+    """
+    import torch
+    ref = Q if Q is not None else K
+    if ref is None:
+        raise ValueError("Q and K are both None")
+    L, d = ref.shape[0], ref.shape[-1]
+    for name, t, ndim in (("Q", Q, 3), ("K", K, 2)):
+        if t is not None and (t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != ndim or t.shape[0] != L
+                              or t.shape[-1] != d or t.device != ref.device):
+            raise ValueError(f"{name}: expected a {ndim}-d bf16 CUDA tensor of the same rows")
+    for name, t, shape, dtype in (("q_weight", q_weight, (d,), torch.bfloat16),
+                                  ("k_weight", k_weight, (d,), torch.bfloat16),
+                                  ("inv_freq", inv_freq, None, torch.float32),
+                                  ("positions", positions, (L,), torch.int32)):
+        if t is not None and (t.dtype != dtype or t.device != ref.device or not t.is_contiguous() or t.dim() != 1
+                              or (shape and tuple(t.shape) != shape)):
+            raise ValueError(f"{name}: expected a contiguous 1-d {dtype} tensor on the same device")
+    H = Q.shape[1] if Q is not None else 1
+    rot = 2 * inv_freq.numel() if inv_freq is not None else 0
+    new = torch.empty if positions is None else torch.zeros
+    Qo = new((L, H, d), dtype=torch.bfloat16, device=ref.device) if Q is not None else None
+    Ko = new((L, d), dtype=torch.bfloat16, device=ref.device) if K is not None else None
+    if L:
+        hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, interleaved, positions, pos0, Qo, Ko,
+                         stream)
+    return Qo, Ko

@@ -21,6 +21,7 @@ EXPORTS = (
     "hsa_select_tokens", "hsa_index", "hsa_sparse_attn", "hsa_decode_workspace_size",
     "hsa_decode_step", "hsa_kernel_launches", "hsa_decode_step_noalloc", "hsa_device_status",
     "hsa_prefill_host_workspace_size", "hsa_prefill_host", "hsa_debug_inject_lost_arrival",
+    "hsa_qk_norm_rope", "hsa_tree_plan", "hsa_tree_workspace_size", "hsa_tree_step", "hsa_tree_commit",
 )
 
 
@@ -69,6 +70,12 @@ def load():
     L.hsa_debug_inject_lost_arrival.argtypes = [ctypes.c_int]
     L.hsa_prefill_host_workspace_size.argtypes = [PP, I64, I64, ctypes.POINTER(SZ)]
     L.hsa_prefill_host.argtypes = [PP, I64, I64, P, P, P, P, P, P, P, P, SZ, P]
+    F32 = ctypes.c_float
+    L.hsa_qk_norm_rope.argtypes = [I64, I32, I32, P, I64, P, I64, P, P, F32, P, I32, I32, P, I64, P, P, P]
+    L.hsa_tree_plan.argtypes = [I32, I32, I64, P, P, P, P, P, P]
+    L.hsa_tree_workspace_size.argtypes = [PP, I32, I32, I64, ctypes.POINTER(SZ)]
+    L.hsa_tree_step.argtypes = [PP, I32, I32, I64] + [P] * 15 + [SZ, P]
+    L.hsa_tree_commit.argtypes = [PP, I32, I32, I64] + [P] * 8
     for name in EXPORTS:
         if name not in ("hsa_status_string", "hsa_kernel_launches"):
             getattr(L, name).restype = ctypes.c_int
@@ -196,3 +203,48 @@ def hsa_decode_step_noalloc(p, batch, capacity, ctx_len, k_idx_cache, K_cache, V
         ctypes.byref(p), batch, capacity, _p(ctx_len), _p(k_idx_cache), _p(K_cache),
         _p(V_cache), _p(ksum_cache), _p(q_idx_new), _p(k_idx_new), _p(Q_new), _p(K_new),
         _p(V_new), _p(O), _p(indices_out), _s(stream)))
+
+
+def hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, interleaved, positions, pos0,
+                     Q_out, K_out, stream=None):
+    """Row strides are the tensors' own; a token's heads and values must be contiguous."""
+    q_stride = k_stride = 0
+    if Q is not None:
+        if Q.stride(-1) != 1 or Q.stride(-2) != d:
+            raise ValueError("Q: the heads of a token must be contiguous")
+        q_stride = Q.stride(0) if L > 1 else H * d
+    if K is not None:
+        if K.stride(-1) != 1:
+            raise ValueError("K: the values of a row must be contiguous")
+        k_stride = K.stride(0) if L > 1 else d
+    _check("hsa_qk_norm_rope", load().hsa_qk_norm_rope(
+        L, H, d, _p(Q), q_stride, _p(K), k_stride, _p(q_weight), _p(k_weight), eps, _p(inv_freq), rot,
+        1 if interleaved else 0, _p(positions), pos0, _p(Q_out), _p(K_out), _s(stream)))
+
+
+def hsa_tree_plan(batch, T, capacity, ctx_len, n_nodes, parents, positions, paths, stream=None):
+    _check("hsa_tree_plan", load().hsa_tree_plan(
+        batch, T, capacity, _p(ctx_len), _p(n_nodes), _p(parents), _p(positions), _p(paths), _s(stream)))
+
+
+def hsa_tree_workspace_size(p, batch, T, capacity) -> int:
+    n = ctypes.c_size_t(0)
+    _check("hsa_tree_workspace_size",
+           load().hsa_tree_workspace_size(ctypes.byref(p), batch, T, capacity, ctypes.byref(n)))
+    return n.value
+
+
+def hsa_tree_step(p, batch, T, capacity, ctx_len, positions, paths, k_idx_cache, K_cache, V_cache, ksum_cache,
+                  q_idx_new, k_idx_new, Q_new, K_new, V_new, O, indices_out, workspace, stream=None):
+    _check("hsa_tree_step", load().hsa_tree_step(
+        ctypes.byref(p), batch, T, capacity, _p(ctx_len), _p(positions), _p(paths), _p(k_idx_cache),
+        _p(K_cache), _p(V_cache), _p(ksum_cache), _p(q_idx_new), _p(k_idx_new), _p(Q_new), _p(K_new),
+        _p(V_new), _p(O), _p(indices_out), _p(workspace), workspace.numel() * workspace.element_size(),
+        _s(stream)))
+
+
+def hsa_tree_commit(p, batch, T, capacity, ctx_len, paths, accepted, k_idx_cache, K_cache, V_cache, ksum_cache,
+                    stream=None):
+    _check("hsa_tree_commit", load().hsa_tree_commit(
+        ctypes.byref(p), batch, T, capacity, _p(ctx_len), _p(paths), _p(accepted), _p(k_idx_cache),
+        _p(K_cache), _p(V_cache), _p(ksum_cache), _s(stream)))

@@ -196,13 +196,15 @@ int hsa_device_status(int reset) {
   if (cudaDeviceSynchronize() != cudaSuccess) return HSA_ERR_CUDA;
   const int a = hsa::attn_wait_flag(reset != 0);
   const int b = hsa::score_wait_flag(reset != 0);
-  if (a < 0 || b < 0) return HSA_ERR_CUDA;
-  return a || b ? HSA_ERR_TIMEOUT : HSA_OK;
+  const int c = hsa::tree_wait_flag(reset != 0);
+  if (a < 0 || b < 0 || c < 0) return HSA_ERR_CUDA;
+  return a || b || c ? HSA_ERR_TIMEOUT : HSA_OK;
 }
 
 int hsa_debug_inject_lost_arrival(int on) {
   if (int e = check_device()) return e;
-  if (!hsa::attn_set_inject(on != 0) || !hsa::score_set_inject(on != 0)) return HSA_ERR_CUDA;
+  if (!hsa::attn_set_inject(on != 0) || !hsa::score_set_inject(on != 0) || !hsa::tree_set_inject(on != 0))
+    return HSA_ERR_CUDA;
   return HSA_OK;
 }
 
@@ -396,10 +398,193 @@ int hsa_decode_step(const hsa_params* p, int32_t batch, int64_t capacity, int32_
   float* opart = reinterpret_cast<float*>(ws + w.opart);
   float* mpart = reinterpret_cast<float*>(ws + w.mpart);
   float* lpart = reinterpret_cast<float*>(ws + w.lpart);
-  if (!hsa::launch_sparse_attn_tc_split(batch, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
-                                        softmax_scale(p), w.parts, opart, mpart, lpart, stream, true))
+  if (!hsa::launch_sparse_attn_tc_split(batch, 1, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
+                                        softmax_scale(p), w.parts, nullptr, opart, mpart, lpart, stream, true))
     return HSA_ERR_CUDA;
   hsa::launch_decode_combine(batch, capacity, ctx_len, p->H, p->d, w.parts, opart, mpart, lpart, O, stream);
+  return launch_status();
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ queries and keys from projections
+
+extern "C" int hsa_qk_norm_rope(int64_t L, int32_t H, int32_t d, const hsa_bf16* Q, int64_t q_stride,
+                                const hsa_bf16* K, int64_t k_stride, const hsa_bf16* q_weight,
+                                const hsa_bf16* k_weight, float eps, const float* inv_freq, int32_t rot,
+                                int32_t interleaved, const int32_t* positions, int64_t pos0, hsa_bf16* Q_out,
+                                hsa_bf16* K_out, cudaStream_t stream) {
+  constexpr int64_t kMax = (int64_t(1) << 31) - 1;
+  if (L < 0 || L > kMax || H < 1 || H > 128 || (d != 64 && d != 128)) return HSA_ERR_ARG;
+  if (rot < 0 || rot > d || rot % 16 || !(eps >= 0.f) || std::isinf(eps)) return HSA_ERR_ARG;
+  if (interleaved != 0 && interleaved != 1) return HSA_ERR_ARG;
+  if (!positions && (pos0 < 0 || pos0 > kMax - L)) return HSA_ERR_ARG;
+  if (L == 0) return HSA_OK;
+  if (!Q && !K) return HSA_ERR_ARG;
+  auto rows_ok = [&](const hsa_bf16* in, const hsa_bf16* w, const hsa_bf16* out, int64_t stride, int64_t n) {
+    return aligned16(in) && aligned16(out) && (!w || aligned16(w)) && stride >= n && stride % 8 == 0 &&
+           stride <= (int64_t(1) << 62) / L;
+  };
+  if (Q && !rows_ok(Q, q_weight, Q_out, q_stride, int64_t(H) * d)) return HSA_ERR_ARG;
+  if (K && !rows_ok(K, k_weight, K_out, k_stride, d)) return HSA_ERR_ARG;
+  const auto word = [](const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
+  if ((rot > 0 && !word(inv_freq)) || (positions && !word(positions))) return HSA_ERR_ARG;
+  if (int e = check_device()) return e;
+  hsa::launch_qk_norm_rope(L, H, d, Q, q_stride, K, k_stride, q_weight, k_weight, eps, inv_freq, rot,
+                           interleaved != 0, positions, pos0, Q_out, K_out, stream);
+  return launch_status();
+}
+
+// ------------------------------------------------------------------ drafted trees
+
+namespace {
+
+// Workspace of a tree step (256-byte aligned regions), rows = batch * T:
+//   n_items i32, rowpos [rows] i32, block-score keys [rows][ldb] u32, tail keys
+//   [rows][tail_ld] u32, kept blocks [rows][m] i32, pairs [rows][m] u32, items
+//   [max_items] int4, token-score keys [rows][m*B] u32, indices [rows][k] i32
+//   (unless the caller takes them), attention parts as in a decode step.
+struct TreeWs {
+  size_t n_items, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, opart, mpart, lpart, total;
+  int64_t rows, ldb, max_items;
+  int parts, tail_ld;
+};
+TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) {
+  TreeWs w{};
+  w.rows = int64_t(batch) * T;
+  w.ldb = capacity / p->B;
+  w.tail_ld = (p->B - 1 + T + 3) / 4 * 4;
+  w.max_items = batch * std::min<int64_t>(int64_t(T) * p->m, w.ldb) * ((p->B + 127) / 128);
+  const int tiles = (p->k + 127) / 128;
+  w.parts = w.rows > 0 ? int(std::max<int64_t>(1, std::min<int64_t>(std::min(tiles, 16), 128 / w.rows))) : 1;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes > 0 ? bytes : 1); return at; };
+  const size_t rows = size_t(w.rows);
+  w.n_items = take(4);
+  w.rowpos = take(rows * 4);
+  w.bkeys = take(rows * w.ldb * 4);
+  w.tail = take(rows * w.tail_ld * 4);
+  w.blocks = take(rows * p->m * 4);
+  w.pairs = take(rows * p->m * 4);
+  w.items = take(size_t(w.max_items) * 16);
+  w.tkeys = take(rows * p->m * p->B * 4);
+  w.idx = take(rows * p->k * 4);
+  const size_t parts = w.parts > 1 ? rows * w.parts : 0;
+  w.opart = take(parts * p->H * p->d * 4);
+  w.mpart = take(parts * p->H * 4);
+  w.lpart = take(parts * p->H * 4);
+  w.total = o;
+  return w;
+}
+
+int check_tree_sizes(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) {
+  constexpr int64_t kMax = (int64_t(1) << 31) - 1;
+  if (batch < 0 || T < 1 || T > HSA_TREE_MAX) return HSA_ERR_ARG;
+  if (capacity < p->B || capacity % p->B || capacity / p->B > kMaxBlocks) return HSA_ERR_ARG;
+  // cache rows and (node, slot) pairs are counted in 32 bits, sequences in 28
+  if (batch > 0 && (capacity > kMax / batch || int64_t(batch) * T > kMax / p->m || batch >= (1 << 28)))
+    return HSA_ERR_ARG;
+  if (int64_t(batch) * T > kMax / p->H) return HSA_ERR_ARG;
+  return HSA_OK;
+}
+
+bool aligned4(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+int hsa_tree_plan(int32_t batch, int32_t T, int64_t capacity, const int32_t* ctx_len, const int32_t* n_nodes,
+                  const int32_t* parents, int32_t* positions, int32_t* paths, cudaStream_t stream) {
+  if (batch < 0 || T < 1 || T > HSA_TREE_MAX || capacity < 1 || capacity > (int64_t(1) << 31) - 1) return HSA_ERR_ARG;
+  if (batch == 0) return HSA_OK;
+  if (!aligned4(ctx_len) || !aligned4(parents) || !aligned4(positions) || !aligned4(paths)) return HSA_ERR_ARG;
+  if (n_nodes && !aligned4(n_nodes)) return HSA_ERR_ARG;
+  if (int e = check_device()) return e;
+  hsa::launch_tree_plan(batch, T, capacity, ctx_len, n_nodes, parents, positions, paths, stream);
+  return launch_status();
+}
+
+int hsa_tree_workspace_size(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity, size_t* bytes) {
+  if (!bytes) return HSA_ERR_ARG;
+  if (int e = check_index_params(p)) return e;
+  if (int e = check_attn_params(p)) return e;
+  if (int e = check_tree_sizes(p, batch, T, capacity)) return e;
+  *bytes = tree_ws(p, batch, T, capacity).total;
+  return HSA_OK;
+}
+
+int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity, const int32_t* ctx_len,
+                  const int32_t* positions, const int32_t* paths, hsa_bf16* k_idx_cache, hsa_bf16* K_cache,
+                  hsa_bf16* V_cache, const float* ksum_cache, const hsa_bf16* q_idx_new, const hsa_bf16* k_idx_new,
+                  const hsa_bf16* Q_new, const hsa_bf16* K_new, const hsa_bf16* V_new, hsa_bf16* O,
+                  int32_t* indices_out, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  size_t need = 0;
+  if (int e = hsa_tree_workspace_size(p, batch, T, capacity, &need)) return e;
+  if (batch == 0) return HSA_OK;
+  const void* ptrs[] = {k_idx_cache, K_cache, V_cache, ksum_cache, q_idx_new, k_idx_new, Q_new, K_new, V_new, O};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return HSA_ERR_ARG;
+  if (!aligned4(ctx_len) || !aligned4(positions) || !aligned4(paths)) return HSA_ERR_ARG;
+  if (indices_out && !aligned16(indices_out)) return HSA_ERR_ARG;
+  if (!aligned16(workspace) || workspace_bytes < need) return HSA_ERR_WORKSPACE;
+  if (int e = check_device()) return e;
+  const TreeWs w = tree_ws(p, batch, T, capacity);
+  char* ws = static_cast<char*>(workspace);
+  int32_t* blocks = reinterpret_cast<int32_t*>(ws + w.blocks);
+  int32_t* idx = indices_out ? indices_out : reinterpret_cast<int32_t*>(ws + w.idx);
+  hsa::TreeArgs a{};
+  a.T = T; a.B = p->B; a.m = p->m; a.k = p->k; a.d = p->d;
+  a.capacity = capacity; a.ldb = w.ldb;
+  a.ctx = ctx_len; a.positions = positions; a.paths = paths;
+  a.k_idx_cache = k_idx_cache; a.K_cache = K_cache; a.V_cache = V_cache; a.ksum_cache = ksum_cache;
+  a.q_new = q_idx_new; a.k_idx_new = k_idx_new; a.K_new = K_new; a.V_new = V_new;
+  a.rowpos = reinterpret_cast<int32_t*>(ws + w.rowpos);
+  a.bkeys = reinterpret_cast<uint32_t*>(ws + w.bkeys);
+  a.tailkeys = reinterpret_cast<uint32_t*>(ws + w.tail);
+  a.tkeys = reinterpret_cast<uint32_t*>(ws + w.tkeys);
+  a.tail_ld = w.tail_ld;
+  a.blocks = blocks;
+  a.pairs = reinterpret_cast<uint32_t*>(ws + w.pairs);
+  a.items = reinterpret_cast<int4*>(ws + w.items);
+  a.n_items = reinterpret_cast<int*>(ws + w.n_items);
+  // A node's row of the selections is at the node's own position; a row that
+  // takes no part has position -1.
+  hsa::RowMap rm{w.rows, capacity, a.rowpos, capacity};
+  // The kernels are programmatic dependent launches, as in a decode step.
+  // 1. drafted rows appended, tails and cached blocks scored; top-m
+  if (!hsa::launch_tree_block_scores(a, batch, p->d_idx, stream)) return HSA_ERR_CUDA;
+  hsa::launch_topm_from_keys(rm, w.rows, a.bkeys, w.ldb, p->B, p->m, w.ldb > 2 ? w.ldb - 2 : 1, blocks, stream, true);
+  // 2. token scores of the kept blocks, each cached block read once for all its nodes; top-k
+  if (!hsa::launch_tree_lists(a, batch, stream)) return HSA_ERR_CUDA;
+  if (!hsa::launch_tree_token_scores(a, batch, p->d_idx, w.max_items, stream)) return HSA_ERR_CUDA;
+  hsa::launch_topk_from_keys(rm, w.rows, blocks, a.tkeys, p->B, p->m, p->k, idx, stream, true);
+  hsa::launch_tree_rows(a, w.rows, idx, stream);
+  // 3. attention over the kept rows
+  float* opart = reinterpret_cast<float*>(ws + w.opart);
+  float* mpart = reinterpret_cast<float*>(ws + w.mpart);
+  float* lpart = reinterpret_cast<float*>(ws + w.lpart);
+  if (!hsa::launch_sparse_attn_tc_split(w.rows, T, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
+                                        softmax_scale(p), w.parts, O, opart, mpart, lpart, stream, true))
+    return HSA_ERR_CUDA;
+  if (w.parts > 1) hsa::launch_tree_combine(w.rows, p->H, p->d, w.parts, opart, mpart, lpart, O, stream);
+  return launch_status();
+}
+
+int hsa_tree_commit(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity, int32_t* ctx_len,
+                    const int32_t* paths, const int32_t* accepted, hsa_bf16* k_idx_cache, hsa_bf16* K_cache,
+                    hsa_bf16* V_cache, float* ksum_cache, cudaStream_t stream) {
+  if (int e = check_index_params(p)) return e;
+  if (int e = check_attn_params(p)) return e;
+  if (int e = check_tree_sizes(p, batch, T, capacity)) return e;
+  if (batch == 0) return HSA_OK;
+  const void* ptrs[] = {k_idx_cache, K_cache, V_cache, ksum_cache};
+  for (const void* q : ptrs)
+    if (!aligned16(q)) return HSA_ERR_ARG;
+  if (!aligned4(ctx_len) || !aligned4(paths) || !aligned4(accepted)) return HSA_ERR_ARG;
+  if (int e = check_device()) return e;
+  hsa::launch_tree_commit(batch, T, capacity, p->B, p->d_idx, p->d, ctx_len, paths, accepted, k_idx_cache, K_cache,
+                          V_cache, ksum_cache, stream);
   return launch_status();
 }
 

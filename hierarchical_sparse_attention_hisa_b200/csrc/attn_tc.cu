@@ -106,7 +106,8 @@ struct Bars {
 }  // namespace
 
 // Work description of one launch. Query q's kept indices are idx[q][0..k);
-// its K/V rows start at row q * kv_stride (0: one K/V shared by all queries).
+// its K/V rows start at row (q / q_per_seq) * kv_stride (stride 0: one K/V
+// shared by all queries).
 // The launch covers heads [h0, h0 + nh) of the H heads of each Q / O row.
 // Each query is cut into items_per_query parts of tiles_per_item 128-key
 // tiles; with one part per query the kernel writes normalised O, otherwise
@@ -122,6 +123,7 @@ struct AttnArgs {
   int Lq, Lk, k, H, h0, nh;
   float scale_log2;
   int64_t kv_stride;
+  int q_per_seq;
   int items_per_query, tiles_per_item;
   uint16_t* O;
   float *Opart, *mpart, *lpart;  // [items][H][d], [items][H], [items][H]
@@ -360,8 +362,9 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
     for (int wi = blockIdx.x; wi < n_items && !dead; wi += gridDim.x, ++qn) {
       const int w = item(wi), q = w / ipq, part = w - q * ipq;
       const int32_t* row = idx + int64_t(q) * k;
-      const uint4* Kq = reinterpret_cast<const uint4*>(K + int64_t(q) * a.kv_stride * DH);
-      const uint4* Vq = reinterpret_cast<const uint4*>(V + int64_t(q) * a.kv_stride * DH);
+      const int64_t kv0 = int64_t(q / a.q_per_seq) * a.kv_stride * DH;
+      const uint4* Kq = reinterpret_cast<const uint4*>(K + kv0);
+      const uint4* Vq = reinterpret_cast<const uint4*>(V + kv0);
       const int4 win = pre;
       if (wi + int(gridDim.x) < n_items) pre = ts.window(idx, item(wi + gridDim.x) / ipq, k);
       const int last = ts.last_valid(win, row, k, Lk);
@@ -809,24 +812,26 @@ bool launch_sparse_attn_tc(int64_t Lq, const void* Q, const void* K, const void*
   a.idx = idx; a.Lq = int(Lq); a.Lk = int(Lk); a.k = k; a.H = H;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.kv_stride = 0;
+  a.q_per_seq = 1;
   a.items_per_query = 1;
   a.tiles_per_item = (k + TILE - 1) / TILE;
   a.O = static_cast<uint16_t*>(O);
   return launch_args(a, d, K, V, s, false, true);
 }
 
-bool launch_sparse_attn_tc_split(int batch, const void* Q, const void* Kc, const void* Vc, const int32_t* idx,
-                                 int64_t capacity, int k, int H, int d, float scale, int parts, float* Opart,
-                                 float* mpart, float* lpart, cudaStream_t s, bool pdl) {
-  if (batch == 0) return true;
+bool launch_sparse_attn_tc_split(int64_t rows, int rows_per_seq, const void* Q, const void* Kc, const void* Vc,
+                                 const int32_t* idx, int64_t capacity, int k, int H, int d, float scale, int parts,
+                                 void* O, float* Opart, float* mpart, float* lpart, cudaStream_t s, bool pdl) {
+  if (rows == 0) return true;
   AttnArgs a{};
   a.Q = static_cast<const uint16_t*>(Q);
-  a.idx = idx; a.Lq = batch; a.Lk = int(capacity); a.k = k; a.H = H;
+  a.idx = idx; a.Lq = int(rows); a.Lk = int(capacity); a.k = k; a.H = H;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.kv_stride = capacity;
+  a.q_per_seq = rows_per_seq;
   a.items_per_query = parts;
   a.tiles_per_item = ((k + TILE - 1) / TILE + parts - 1) / parts;
-  a.O = nullptr;
+  a.O = parts == 1 ? static_cast<uint16_t*>(O) : nullptr;
   a.Opart = Opart; a.mpart = mpart; a.lpart = lpart;
   // parts of at most a few tiles: the per-tile vote costs less there than a second launch
   return launch_args(a, d, Kc, Vc, s, pdl, false);

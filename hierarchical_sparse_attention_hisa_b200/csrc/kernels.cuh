@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "hsa.h"
 
 namespace hsa {
 
@@ -73,9 +74,48 @@ void launch_decode_token_scores(int batch, int64_t capacity, const int32_t* ctx,
 // (also advances ctx: every sequence that took the step grows by one token)
 void launch_decode_combine(int batch, int64_t capacity, int32_t* ctx, int H, int d, int parts,
                            const float* Opart, const float* mpart, const float* lpart, void* O, cudaStream_t s);
-bool launch_sparse_attn_tc_split(int batch, const void* Q, const void* Kc, const void* Vc, const int32_t* idx,
-                                 int64_t capacity, int k, int H, int d, float scale, int parts, float* Opart,
-                                 float* mpart, float* lpart, cudaStream_t s, bool pdl = false);
+// Attention of `rows` queries, rows_per_seq of them over each sequence's cache of `capacity` rows, each
+// cut into `parts`. With one part and O given the kernel writes O; otherwise it writes the parts.
+bool launch_sparse_attn_tc_split(int64_t rows, int rows_per_seq, const void* Q, const void* Kc, const void* Vc,
+                                 const int32_t* idx, int64_t capacity, int k, int H, int d, float scale, int parts,
+                                 void* O, float* Opart, float* mpart, float* lpart, cudaStream_t s, bool pdl = false);
+
+// Per-head RMS norm and rotation of queries [L][H][d] and keys [L][d] (either may be null).
+void launch_qk_norm_rope(int64_t L, int H, int d, const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
+                         const void* qw, const void* kw, float eps, const float* inv_freq, int rot, bool interleaved,
+                         const int32_t* positions, int64_t pos0, void* Qo, void* Ko, cudaStream_t s);
+
+// Drafted trees (tree_kernels.cu, tree_scores.cu): T nodes per sequence, row = sequence * T + node.
+constexpr int kTreeMax = HSA_TREE_MAX;
+struct TreeArgs {
+  int T, B, m, k, d;
+  int64_t capacity, ldb;           // ldb: row length of bkeys
+  const int32_t *ctx, *positions, *paths;
+  uint16_t *k_idx_cache, *K_cache, *V_cache;
+  const float* ksum_cache;
+  const uint16_t *q_new, *k_idx_new, *K_new, *V_new;
+  int32_t* rowpos;                 // [rows] position of each node that takes part, else -1
+  uint32_t *bkeys, *tailkeys, *tkeys;  // [rows][ldb], [rows][tail_ld], [rows][m][B]
+  int tail_ld;
+  const int32_t* blocks;           // [rows][m]
+  uint32_t* pairs;                 // [rows][m]: node << 16 | slot
+  int4* items;                     // (first key row, first pair, pairs | key rows << 16, sequence << 3 | 128-row piece)
+  int* n_items;
+};
+void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, const int32_t* n_nodes,
+                      const int32_t* parents, int32_t* positions, int32_t* paths, cudaStream_t s);
+// (also appends the drafted rows to the caches and scores every node's tail)
+bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStream_t s);
+bool launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s);
+bool launch_tree_token_scores(const TreeArgs& a, int batch, int d_idx, int64_t max_items, cudaStream_t s);
+void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s);
+void launch_tree_combine(int64_t rows, int H, int d, int parts, const float* Opart, const float* mpart,
+                         const float* lpart, void* O, cudaStream_t s);
+void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,
+                        const int32_t* paths, const int32_t* accepted, void* k_idx_cache, void* K_cache,
+                        void* V_cache, float* ksum_cache, cudaStream_t s);
+int tree_wait_flag(bool reset);
+bool tree_set_inject(bool on);
 
 // Sticky per-device flags set by a bounded wait that gave up (1), read on the
 // host with a synchronous copy and optionally cleared; -1 on a CUDA error.

@@ -993,8 +993,9 @@ void launch_topk_from_keys(RowMap rm, int64_t rows, const int32_t* blocks, const
     cudaFuncSetAttribute(topk_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(RowSmem)));
     launch_kernel(pdl, topk_rows_kernel, unsigned(rows), kRowNT, sizeof(RowSmem), s, rm, blocks, tkeys, B, m, k,
                   indices);
-  } else if (rows < 2 * num_sms()) {
-    // few longer rows (a decode batch): wide CTAs cut each row's latency
+  } else if (rows < 2 * num_sms() || (int64_t(m) * B) % 4 != 0) {
+    // few longer rows (a decode batch): wide CTAs cut each row's latency. Also
+    // rows that do not all start on 16 bytes, which the warp form loads by.
 #define HSA_TOPK(K) \
   launch_kernel(pdl, topk_from_keys_kernel<1024, K>, unsigned(rows), 1024, 0, s, rm, blocks, tkeys, B, m, k, indices)
     int kpt = 1;

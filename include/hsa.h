@@ -241,13 +241,111 @@ HSA_API int hsa_decode_step_noalloc(const hsa_params* p, int32_t batch, int64_t 
                                     const hsa_bf16* V_new, hsa_bf16* O, int32_t* indices_out,
                                     cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Queries and keys from a layer's projections. The pages start from finished
+ * queries and keys; this call makes them, for the attention (Q [L][H][d],
+ * K [L][d]) and, with H = 1 and d = d_idx, for the indexer.
+ * --------------------------------------------------------------------------- */
+
+/* RMS norm of every query head and of the key, then the rotation by the
+ * row's position, in one pass:
+ *   y = x * weight / sqrt(mean(x^2) + eps)   over the d values of a head,
+ *   pairs (a, b) of y's first `rot` values turned by u = position * inv_freq[i]:
+ *   (a cos u - b sin u, b cos u + a sin u); pair i is (i, i + rot/2), or
+ *   (2i, 2i + 1) with interleaved = 1. The other values stay as they are.
+ * fp32 throughout (u in fp64), rounded once to bf16.
+ *   Q      [L][H][d] bf16, token rows q_stride values apart (a multiple of 8,
+ *          >= H*d: e.g. the rows of a fused projection), or NULL: keys only;
+ *   K      [L][d] bf16, rows k_stride apart (a multiple of 8, >= d), or NULL:
+ *          queries only;
+ *   q_weight, k_weight [d] bf16, shared by all heads; NULL: all ones;
+ *   inv_freq [rot/2] fp32, device memory (unused with rot = 0, no rotation);
+ *   rot    a multiple of 16, 0 <= rot <= d;  d 64 or 128;  1 <= H <= 128;
+ *   positions [L] int32 (e.g. ctx_len for a decode step, the positions of
+ *          hsa_tree_plan for a drafted tree), or NULL: row i is at pos0 + i.
+ *          A row with a negative position is left unwritten;
+ *   Q_out  [L][H][d], K_out [L][d] bf16, dense. Each may be its input if that
+ *          is dense too; otherwise outputs must not overlap inputs.
+ * pos0 >= 0 and pos0 + L < 2^31 (ignored with positions). One launch. */
+HSA_API int hsa_qk_norm_rope(int64_t L, int32_t H, int32_t d, const hsa_bf16* Q, int64_t q_stride,
+                             const hsa_bf16* K, int64_t k_stride, const hsa_bf16* q_weight,
+                             const hsa_bf16* k_weight, float eps, const float* inv_freq,
+                             int32_t rot, int32_t interleaved, const int32_t* positions,
+                             int64_t pos0, hsa_bf16* Q_out, hsa_bf16* K_out, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Drafted trees: the decode step for a tree of drafted tokens per sequence
+ * (speculative decoding). The pages describe no such interface. Node i of a
+ * sequence's tree is a drafted token whose parent is an earlier node, or the
+ * sequence's last cached token; its path is its ancestors and itself. One
+ * round: hsa_tree_plan once, hsa_tree_step in every layer, and once the caller
+ * has chosen which path it accepts, hsa_tree_commit in every layer.
+ * --------------------------------------------------------------------------- */
+#define HSA_TREE_MAX 64 /* drafted nodes per sequence */
+
+/* Positions and paths of `batch` trees of up to T nodes (1 <= T <= HSA_TREE_MAX).
+ *   ctx_len   [batch] int32: cached tokens per sequence;
+ *   n_nodes   [batch] int32: nodes of each tree (clamped to [0, T]), or NULL: T;
+ *   parents   [batch][T] int32: -1 (a child of the last cached token) or an
+ *             earlier node, parents[i] < i;
+ *   positions [batch][T] int32, written: ctx_len + depth, or -1 for a node that
+ *             takes no part: one behind its tree's nodes, one whose path breaks
+ *             the rule above, every node of a sequence with ctx_len < 0 or
+ *             ctx_len + n_nodes > capacity;
+ *   paths     [batch][T][T] int32, written: the node's path from the root down,
+ *             -1 after it (and everywhere for a node that takes no part). */
+HSA_API int hsa_tree_plan(int32_t batch, int32_t T, int64_t capacity, const int32_t* ctx_len,
+                          const int32_t* n_nodes, const int32_t* parents, int32_t* positions,
+                          int32_t* paths, cudaStream_t stream);
+
+/* Workspace bytes for hsa_tree_step. */
+HSA_API int hsa_tree_workspace_size(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity,
+                                    size_t* bytes);
+
+/* One layer's verification of the drafted trees: for every node, selection
+ * and attention as hsa_decode_step would do them for its token had the tokens
+ * of its path been appended one by one.
+ * Caches and new rows are those of hsa_decode_step, with T rows per sequence
+ * in place of one: q_idx_new/k_idx_new [batch][T][d_idx], Q_new and O
+ * [batch][T][H][d], K_new/V_new [batch][T][d] (bf16); positions and paths are
+ * hsa_tree_plan's for the same ctx_len.
+ * The drafted rows are written to the caches behind the cached ones, node i of
+ * sequence b to row ctx_len[b] + i; rows < ctx_len, the block sums and ctx_len
+ * stay as they are, so the next hsa_decode_step or hsa_tree_step overwrites the
+ * drafted rows. indices_out [batch][T][k] int32, or NULL: the kept cache rows
+ * of each node, ascending, -1 padded (an entry below ctx_len is that position,
+ * entry ctx_len + j is drafted node j). A node that takes no part writes
+ * nothing to the caches; its O row is zero and its indices are -1.
+ * batch * capacity, batch * T * m and batch * T * H must stay below 2^31, and
+ * capacity / B is at most 16384 blocks. Calls that may overlap on the GPU
+ * (other streams, several captured graphs) need workspaces of their own. */
+HSA_API int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity,
+                          const int32_t* ctx_len, const int32_t* positions, const int32_t* paths,
+                          hsa_bf16* k_idx_cache, hsa_bf16* K_cache, hsa_bf16* V_cache,
+                          const float* ksum_cache, const hsa_bf16* q_idx_new,
+                          const hsa_bf16* k_idx_new, const hsa_bf16* Q_new, const hsa_bf16* K_new,
+                          const hsa_bf16* V_new, hsa_bf16* O, int32_t* indices_out, void* workspace,
+                          size_t workspace_bytes, cudaStream_t stream);
+
+/* Accepts the path of one node per sequence after hsa_tree_step: its tokens'
+ * rows move to cache rows ctx_len, ctx_len + 1, ... (k_idx, K and V), the sums
+ * of the blocks they complete are written, and ctx_len[b] grows by the path's
+ * length.
+ *   accepted [batch] int32: the last accepted node, or -1 for none. A sequence
+ *   whose entry is no node of the plan is left as it is.
+ * Of p, B, d_idx and d are used. One launch. */
+HSA_API int hsa_tree_commit(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity,
+                            int32_t* ctx_len, const int32_t* paths, const int32_t* accepted,
+                            hsa_bf16* k_idx_cache, hsa_bf16* K_cache, hsa_bf16* V_cache,
+                            float* ksum_cache, cudaStream_t stream);
+
 /* Number of kernels this library has launched in the calling process (all
  * devices, all streams) since it was loaded. A diagnostic counter for
  * benchmarks and tests; it is not synchronised with the GPU. */
 HSA_API uint64_t hsa_kernel_launches(void);
 
 /* Whether a bounded device-side wait has given up on the current device.
- * The tensor-core kernels (block/token scoring, attention) bound every wait
+ * The tensor-core kernels (block/token/tree scoring, attention) bound every wait
  * on an mbarrier to about two seconds of SM clock. A wait that runs out sets
  * a sticky per-device flag; the kernel then skips the work that depended on
  * the wait and runs to completion, so that launch's outputs are incomplete,
@@ -262,7 +360,7 @@ HSA_API int hsa_device_status(int reset);
 
 /* Test hook for the bounded-wait machinery, not for production use. The pages
  * describe no such interface. With on != 0, on the current device: every
- * bounded wait of the tensor-core kernels (block/token scoring, attention)
+ * bounded wait of the tensor-core kernels (block/token/tree scoring, attention)
  * gives up after about a millisecond instead of about two seconds, and the
  * next launch of each of them loses one producer hand-off in its first CTA
  * (the scoring kernels skip producing their first tile; the attention's first
