@@ -111,16 +111,14 @@ def params(B=128, m=64, k=2048, d_idx=128, H=64, d=128, scale=0.0) -> hsa_params
 
 def _p(t):
     """Data pointer of a tensor (None -> NULL); 0-size tensors pass NULL."""
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr()) if t.numel() else None
+    return None if t is None else t.data_ptr() or None
 
 
 def _s(stream):
-    if stream is None:
+    if stream is None:  # the current device's current stream, without building a Stream object (about 1 us a call)
         import torch
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(fn, status):
