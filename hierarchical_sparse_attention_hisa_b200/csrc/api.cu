@@ -398,8 +398,8 @@ int hsa_decode_step(const hsa_params* p, int32_t batch, int64_t capacity, int32_
   float* opart = reinterpret_cast<float*>(ws + w.opart);
   float* mpart = reinterpret_cast<float*>(ws + w.mpart);
   float* lpart = reinterpret_cast<float*>(ws + w.lpart);
-  if (!hsa::launch_sparse_attn_tc_split(batch, 1, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
-                                        softmax_scale(p), w.parts, nullptr, opart, mpart, lpart, stream, true))
+  if (!hsa::launch_sparse_attn_tc_split(batch, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
+                                        softmax_scale(p), w.parts, opart, mpart, lpart, stream, true))
     return HSA_ERR_CUDA;
   hsa::launch_decode_combine(batch, capacity, ctx_len, p->H, p->d, w.parts, opart, mpart, lpart, O, stream);
   return launch_status();
@@ -440,14 +440,16 @@ extern "C" int hsa_qk_norm_rope(int64_t L, int32_t H, int32_t d, const hsa_bf16*
 namespace {
 
 // Workspace of a tree step (256-byte aligned regions), rows = batch * T:
-//   n_items i32, rowpos [rows] i32, block-score keys [rows][ldb] u32, tail keys
-//   [rows][tail_ld] u32, kept blocks [rows][m] i32, pairs [rows][m] u32, items
-//   [max_items] int4, token-score keys [rows][m*B] u32, indices [rows][k] i32
-//   (unless the caller takes them), attention parts as in a decode step.
+//   counters [2] i32, rowpos [rows] i32, block-score keys [rows][ldb] u32, tail
+//   keys [rows][tail_ld] u32, kept blocks [rows][m] i32, pairs [rows][m] u32,
+//   items [max_items] int4, token-score keys [rows][m*B] u32, indices [rows][k]
+//   i32 (unless the caller takes them), the attention's items, their CTAs' first
+//   ones and the rows' parts, and the parts: O f32, maxima and row sums f32.
 struct TreeWs {
-  size_t n_items, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, opart, mpart, lpart, total;
+  size_t counters, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, aitems, cta, rparts, opart, mpart, lpart,
+      total;
   int64_t rows, ldb, max_items;
-  int parts, tail_ld;
+  int tail_ld;
 };
 TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) {
   TreeWs w{};
@@ -455,12 +457,10 @@ TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) 
   w.ldb = capacity / p->B;
   w.tail_ld = (p->B - 1 + T + 3) / 4 * 4;
   w.max_items = batch * std::min<int64_t>(int64_t(T) * p->m, w.ldb) * ((p->B + 127) / 128);
-  const int tiles = (p->k + 127) / 128;
-  w.parts = w.rows > 0 ? int(std::max<int64_t>(1, std::min<int64_t>(std::min(tiles, 16), 128 / w.rows))) : 1;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes > 0 ? bytes : 1); return at; };
   const size_t rows = size_t(w.rows);
-  w.n_items = take(4);
+  w.counters = take(8);
   w.rowpos = take(rows * 4);
   w.bkeys = take(rows * w.ldb * 4);
   w.tail = take(rows * w.tail_ld * 4);
@@ -469,7 +469,11 @@ TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) 
   w.items = take(size_t(w.max_items) * 16);
   w.tkeys = take(rows * p->m * p->B * 4);
   w.idx = take(rows * p->k * 4);
-  const size_t parts = w.parts > 1 ? rows * w.parts : 0;
+  // a CTA's list has at most two rows that it shares with its neighbours
+  const size_t parts = 2 * hsa::kGivenItemCtas;
+  w.aitems = take((rows + hsa::kGivenItemCtas) * 16);
+  w.cta = take((hsa::kGivenItemCtas + 1) * 4);
+  w.rparts = take(rows * 8);
   w.opart = take(parts * p->H * p->d * 4);
   w.mpart = take(parts * p->H * 4);
   w.lpart = take(parts * p->H * 4);
@@ -547,7 +551,10 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   a.blocks = blocks;
   a.pairs = reinterpret_cast<uint32_t*>(ws + w.pairs);
   a.items = reinterpret_cast<int4*>(ws + w.items);
-  a.n_items = reinterpret_cast<int*>(ws + w.n_items);
+  a.counters = reinterpret_cast<int*>(ws + w.counters);
+  a.attn_items = reinterpret_cast<int4*>(ws + w.aitems);
+  a.cta_items = reinterpret_cast<int*>(ws + w.cta);
+  a.row_parts = reinterpret_cast<int2*>(ws + w.rparts);
   // A node's row of the selections is at the node's own position; a row that
   // takes no part has position -1.
   hsa::RowMap rm{w.rows, capacity, a.rowpos, capacity};
@@ -556,18 +563,18 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   if (!hsa::launch_tree_block_scores(a, batch, p->d_idx, stream)) return HSA_ERR_CUDA;
   hsa::launch_topm_from_keys(rm, w.rows, a.bkeys, w.ldb, p->B, p->m, w.ldb > 2 ? w.ldb - 2 : 1, blocks, stream, true);
   // 2. token scores of the kept blocks, each cached block read once for all its nodes; top-k
-  if (!hsa::launch_tree_lists(a, batch, stream)) return HSA_ERR_CUDA;
+  hsa::launch_tree_lists(a, batch, stream);
   if (!hsa::launch_tree_token_scores(a, batch, p->d_idx, w.max_items, stream)) return HSA_ERR_CUDA;
   hsa::launch_topk_from_keys(rm, w.rows, blocks, a.tkeys, p->B, p->m, p->k, idx, stream, true);
   hsa::launch_tree_rows(a, w.rows, idx, stream);
-  // 3. attention over the kept rows
+  // 3. attention over the kept rows, in equal shares of 128-key tiles per CTA
   float* opart = reinterpret_cast<float*>(ws + w.opart);
   float* mpart = reinterpret_cast<float*>(ws + w.mpart);
   float* lpart = reinterpret_cast<float*>(ws + w.lpart);
-  if (!hsa::launch_sparse_attn_tc_split(w.rows, T, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
-                                        softmax_scale(p), w.parts, O, opart, mpart, lpart, stream, true))
+  if (!hsa::launch_sparse_attn_tc_items(w.rows, T, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
+                                        softmax_scale(p), a.attn_items, a.cta_items, O, opart, mpart, lpart, stream))
     return HSA_ERR_CUDA;
-  if (w.parts > 1) hsa::launch_tree_combine(w.rows, p->H, p->d, w.parts, opart, mpart, lpart, O, stream);
+  hsa::launch_tree_combine(a, w.rows, p->H, opart, mpart, lpart, O, stream);
   return launch_status();
 }
 

@@ -74,11 +74,16 @@ void launch_decode_token_scores(int batch, int64_t capacity, const int32_t* ctx,
 // (also advances ctx: every sequence that took the step grows by one token)
 void launch_decode_combine(int batch, int64_t capacity, int32_t* ctx, int H, int d, int parts,
                            const float* Opart, const float* mpart, const float* lpart, void* O, cudaStream_t s);
-// Attention of `rows` queries, rows_per_seq of them over each sequence's cache of `capacity` rows, each
-// cut into `parts`. With one part and O given the kernel writes O; otherwise it writes the parts.
-bool launch_sparse_attn_tc_split(int64_t rows, int rows_per_seq, const void* Q, const void* Kc, const void* Vc,
-                                 const int32_t* idx, int64_t capacity, int k, int H, int d, float scale, int parts,
-                                 void* O, float* Opart, float* mpart, float* lpart, cudaStream_t s, bool pdl = false);
+bool launch_sparse_attn_tc_split(int batch, const void* Q, const void* Kc, const void* Vc, const int32_t* idx,
+                                 int64_t capacity, int k, int H, int d, float scale, int parts, float* Opart,
+                                 float* mpart, float* lpart, cudaStream_t s, bool pdl = false);
+// Attention of `rows` queries, rows_per_seq of them over each sequence's cache of `capacity` rows, as
+// kGivenItemCtas lists of items (query, first 128-key tile, tiles, part or -1 to write O).
+constexpr int kGivenItemCtas = 148;
+bool launch_sparse_attn_tc_items(int64_t rows, int rows_per_seq, const void* Q, const void* Kc, const void* Vc,
+                                 const int32_t* idx, int64_t capacity, int k, int H, int d, float scale,
+                                 const int4* items, const int* cta_items, void* O, float* Opart, float* mpart,
+                                 float* lpart, cudaStream_t s);
 
 // Per-head RMS norm and rotation of queries [L][H][d] and keys [L][d] (either may be null).
 void launch_qk_norm_rope(int64_t L, int H, int d, const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
@@ -98,18 +103,23 @@ struct TreeArgs {
   uint32_t *bkeys, *tailkeys, *tkeys;  // [rows][ldb], [rows][tail_ld], [rows][m][B]
   int tail_ld;
   const int32_t* blocks;           // [rows][m]
-  uint32_t* pairs;                 // [rows][m]: node << 16 | slot
+  uint32_t* pairs;                 // [rows * m]: node << 16 | slot
   int4* items;                     // (first key row, first pair, pairs | key rows << 16, sequence << 3 | 128-row piece)
-  int* n_items;
+  int* counters;                   // [2]: items, pairs
+  // the attention's work: items and each CTA's first (see launch_sparse_attn_tc_items), and of each row
+  // its first part and how many (0: nothing kept, 1: none, the row is written whole)
+  int4* attn_items;
+  int* cta_items;                  // [kGivenItemCtas + 1]
+  int2* row_parts;                 // [rows]
 };
 void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, const int32_t* n_nodes,
                       const int32_t* parents, int32_t* positions, int32_t* paths, cudaStream_t s);
 // (also appends the drafted rows to the caches and scores every node's tail)
 bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStream_t s);
-bool launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s);
+void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s);
 bool launch_tree_token_scores(const TreeArgs& a, int batch, int d_idx, int64_t max_items, cudaStream_t s);
 void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s);
-void launch_tree_combine(int64_t rows, int H, int d, int parts, const float* Opart, const float* mpart,
+void launch_tree_combine(const TreeArgs& a, int64_t rows, int H, const float* Opart, const float* mpart,
                          const float* lpart, void* O, cudaStream_t s);
 void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,
                         const int32_t* paths, const int32_t* accepted, void* k_idx_cache, void* K_cache,

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kNT) tree_block_scores_kernel(const TreeArgs a
   griddep_wait();
   griddep_launch();
   const int64_t b = blockIdx.x;
-  if (b == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.n_items = 0;
+  if (b == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
   if (int(blockIdx.y) < chunks)
     cached_block_scores<DI, TP>(a, b, blockIdx.y, smem_f);
   else
@@ -241,41 +241,95 @@ __global__ void __launch_bounds__(kNT) tree_block_scores_kernel(const TreeArgs a
 }
 
 // ---------------------------------------------------------------------------
-// Work lists of the token scores, one CTA per sequence: the (node, slot)
-// pairs of each kept cached block, and an item per 128 rows of such a block.
-// The order of items and of pairs inside one is not fixed (atomics); each
-// writes its own keys, so results do not depend on it. Kept tail blocks take
-// their keys from the tail's scores here.
+// Work lists, one launch.
+//
+// Token scores: CTA (sequence, range of 512 cached blocks), a thread per block:
+// the (node, slot) pairs of each kept block and an item per 128 rows of such a
+// block. The order of items and of pairs inside one is not fixed (atomics);
+// each writes its own keys, so results do not depend on it. Kept tail blocks
+// take their keys from the tail's scores here.
+//
+// Attention: one more CTA cuts all rows' 128-key tiles, in row order, into
+// kGivenItemCtas equal shares (what a row keeps follows from its position
+// alone). A static row per CTA leaves most SMs idle when trees are ragged; with
+// equal shares at most two rows of a CTA are cut, whose parts are combined.
 // ---------------------------------------------------------------------------
 constexpr int kListNT = 512;
 
-__global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a) {
-  extern __shared__ __align__(16) int hist[];  // [blocks]: pair counts, then cursors
+HSA_DEV void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
+  const int tid = threadIdx.x;
+  auto tiles_of = [&](int64_t row) -> int {
+    if (row >= rows) return 0;
+    const int64_t t = a.rowpos[row];
+    if (t < 0) return 0;
+    const int64_t nb = t / a.B + 1;
+    const int64_t n = nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1;
+    return int((min(n, int64_t(a.k)) + 127) / 128);
+  };
+  int64_t total = 0;
+  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
+    int sum;
+    block_exclusive_scan<kListNT>(tiles_of(r0 + tid), s_tmp, &sum);
+    total += sum;
+  }
+  const int64_t quota = max(int64_t(1), (total + kGivenItemCtas - 1) / kGivenItemCtas);
+  int64_t tile0 = 0;
+  int item0 = 0, part0 = 0;
+  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
+    const int64_t row = r0 + tid;
+    const int n = tiles_of(row);
+    int sum, items, parts;
+    const int64_t s = tile0 + block_exclusive_scan<kListNT>(n, s_tmp, &sum);
+    const int64_t c0 = s / quota;
+    const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
+    int at = item0 + block_exclusive_scan<kListNT>(pieces, s_tmp, &items);
+    const int part = part0 + block_exclusive_scan<kListNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
+    if (row < rows) a.row_parts[row] = make_int2(part, pieces);
+    for (int j = 0; j < pieces; ++j, ++at) {
+      const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
+      a.attn_items[at] = make_int4(int(row), int(lo - s), int(hi - lo), pieces > 1 ? part + j : -1);
+      if (lo == (c0 + j) * quota) a.cta_items[c0 + j] = at;  // the first item of CTA c0 + j
+    }
+    tile0 += sum;
+    item0 += items;
+    part0 += parts;
+  }
+  for (int64_t c = (total + quota - 1) / quota + tid; c <= kGivenItemCtas; c += kListNT) a.cta_items[c] = item0;
+}
+
+__global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, int64_t rows, int ranges) {
+  __shared__ int hist[kListNT];  // pair counts of this range's blocks, then cursors
   __shared__ int s_tmp[kListNT / 32 + 1];
-  __shared__ int s_base;
+  __shared__ int s_base[2];
   __shared__ int pos_s[kTreeMax];
   griddep_wait();
   griddep_launch();
-  const int64_t b = blockIdx.x;
+  if (blockIdx.x == gridDim.x - 1) {
+    attn_shares(a, rows, s_tmp);
+    return;
+  }
+  const int64_t b = blockIdx.x / ranges;
+  const int range = int(blockIdx.x % ranges);
   const int64_t c = a.ctx[b];
   if (c < 0 || c >= a.capacity) return;
   const int f = int(c / a.B);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lo = range * kListNT, mine = lo + tid;  // this thread's block
   if (tid < a.T) {
     const int t = a.rowpos[b * a.T + tid];
     pos_s[tid] = t >= 0 && needs_scores(t, a.B, a.m, a.k) ? t : -1;
   }
-  for (int e = tid; e < f; e += kListNT) hist[e] = 0;
+  hist[tid] = 0;
   __syncthreads();
   const int32_t* blocks = a.blocks + b * a.T * a.m;
   const int entries = a.T * a.m;
+  const int end = min(f, lo + kListNT);
   for (int e = tid; e < entries; e += kListNT) {
-    if (pos_s[e / a.m] < 0) continue;
     const int blk = blocks[e];
-    if (blk >= 0 && blk < f) atomicAdd(&hist[blk], 1);
+    if (blk >= lo && blk < end && pos_s[e / a.m] >= 0) atomicAdd(&hist[blk - lo], 1);
   }
-  // tail blocks: their keys, a warp per node
-  for (int i = warp; i < a.T; i += kListNT / 32) {
+  // tail blocks: their keys, a warp per node, the nodes spread over the ranges
+  for (int i = range + warp * ranges; i < a.T; i += kListNT / 32 * ranges) {
     const int t = pos_s[i];
     if (t < 0) continue;
     const int64_t row = b * a.T + i;
@@ -291,88 +345,92 @@ __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a) {
     }
   }
   __syncthreads();
-  // this sequence's items: `per` for each block with a pair
+  // this range's items: `per` for each block with a pair
   const int per = (a.B + 127) / 128;
-  const int span = (f + kListNT - 1) / kListNT;
-  const int lo = min(f, tid * span), hi = min(f, lo + span);
-  int np = 0, ni = 0;
-  for (int e = lo; e < hi; ++e) { np += hist[e]; ni += hist[e] > 0; }
+  const int cnt = hist[tid];
   int tot_p, tot_i;
-  int at_p = block_exclusive_scan<kListNT>(np, s_tmp, &tot_p);
-  int at_i = block_exclusive_scan<kListNT>(ni, s_tmp, &tot_i);
-  if (tid == 0) s_base = tot_i ? atomicAdd(a.n_items, tot_i * per) : 0;
+  const int at_p = block_exclusive_scan<kListNT>(cnt, s_tmp, &tot_p);
+  const int at_i = block_exclusive_scan<kListNT>(cnt > 0, s_tmp, &tot_i);
+  if (tot_p == 0) return;
+  if (tid == 0) s_base[0] = atomicAdd(a.counters, tot_i * per);
+  if (tid == 32) s_base[1] = atomicAdd(a.counters + 1, tot_p);
+  hist[tid] = at_p;
   __syncthreads();
-  int4* items = a.items + s_base;
-  for (int e = lo; e < hi; ++e) {
-    const int cnt = hist[e];
-    hist[e] = at_p;
-    if (cnt) {
-      for (int ch = 0; ch < per; ++ch)
-        items[at_i * per + ch] = make_int4(int(b * a.capacity) + e * a.B + 128 * ch, int(b * entries) + at_p,
-                                           cnt | (min(128, a.B - 128 * ch) << 16), int(b << 3) | ch);
-      at_i += 1;
-    }
-    at_p += cnt;
-  }
-  __syncthreads();
-  uint32_t* pairs = a.pairs + b * entries;
+  uint32_t* pairs = a.pairs + s_base[1];
+  if (cnt)
+    for (int ch = 0; ch < per; ++ch)
+      a.items[s_base[0] + at_i * per + ch] =
+          make_int4(int(b * a.capacity) + mine * a.B + 128 * ch, s_base[1] + at_p,
+                    cnt | (min(128, a.B - 128 * ch) << 16), int(b << 3) | ch);
   for (int e = tid; e < entries; e += kListNT) {
-    const int i = e / a.m;
-    if (pos_s[i] < 0) continue;
-    const int blk = blocks[e];
-    if (blk >= 0 && blk < f) pairs[atomicAdd(&hist[blk], 1)] = uint32_t(i) << 16 | uint32_t(e - i * a.m);
+    const int blk = blocks[e], i = e / a.m;
+    if (blk >= lo && blk < end && pos_s[i] >= 0)
+      pairs[atomicAdd(&hist[blk - lo], 1)] = uint32_t(i) << 16 | uint32_t(e - i * a.m);
   }
 }
 
-// Kept positions of each node -> rows of its sequence's cache, in place.
-__global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int32_t* __restrict__ idx) {
-  __shared__ int path[kTreeMax];
+// Kept positions of each node -> rows of its sequence's cache, in place, a warp
+// per node. Positions ascend, so the drafted ones are the last of the list: at
+// most T, found from its end.
+__global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int64_t rows, int32_t* __restrict__ idx) {
   griddep_wait();
   griddep_launch();
-  const int64_t row = blockIdx.x, b = row / a.T;
-  const int t = a.rowpos[row];
-  const int c = a.ctx[b];
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int64_t t = a.rowpos[row];
   if (t < 0) return;  // no part: its entries are -1
-  if (threadIdx.x <= t - c) path[threadIdx.x] = min(max(a.paths[row * a.T + threadIdx.x], 0), a.T - 1);
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.k; e += 256) {
-    const int p = idx[row * a.k + e];
-    if (p >= c) idx[row * a.k + e] = c + path[p - c];
+  const int c = a.ctx[row / a.T];
+  const int64_t nb = t / a.B + 1;
+  const int64_t n = min(int64_t(a.k), nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1);
+  const int32_t* path = a.paths + row * a.T;
+  int32_t* out = idx + row * a.k;
+  for (int64_t e0 = n - 32; e0 > -32; e0 -= 32) {
+    const int64_t e = e0 + lane;
+    const int p = e >= 0 ? out[e] : -1;
+    const bool late = p >= c;
+    if (late) out[e] = c + min(max(path[min(p - c, a.T - 1)], 0), a.T - 1);
+    if (!__all_sync(kFull, late)) break;
   }
 }
 
-// O[row][h][:] from the parts of a split query (as the decode step's
-// combination: with M the largest part maximum, O = sum_p 2^(m_p - M) O_p /
-// sum_p 2^(m_p - M) l_p in log2 units).
-__global__ void tree_combine_kernel(int H, int D, int parts, const float* __restrict__ Opart,
-                                    const float* __restrict__ mpart, const float* __restrict__ lpart,
-                                    uint16_t* __restrict__ O) {
+// O of the rows that were cut (with M the largest part maximum, O = sum_p
+// 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), and of the rows that
+// keep nothing (zero). Grid (row, heads / HPC), a thread per four values.
+template <int D>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int H, const float* __restrict__ Opart,
+                                                           const float* __restrict__ mpart,
+                                                           const float* __restrict__ lpart, uint16_t* __restrict__ O) {
+  constexpr int TPH = D / 4, HPC = 256 / TPH;  // threads per head, heads per CTA
   griddep_wait();
   griddep_launch();
-  const int64_t row = blockIdx.x / H;
-  const int h = int(blockIdx.x % H);
-  constexpr int PMAX = 16;
-  float lv[PMAX], mv[PMAX], ov[PMAX];
-#pragma unroll
-  for (int p = 0; p < PMAX; ++p)
-    if (p < parts) {
-      const int64_t w = row * parts + p;
-      lv[p] = lpart[w * H + h];
-      mv[p] = mpart[w * H + h];
-      ov[p] = Opart[(w * H + h) * D + threadIdx.x];
-    }
-  float M = -INFINITY, num = 0.f, den = 0.f;
-#pragma unroll
-  for (int p = 0; p < PMAX; ++p)
-    if (p < parts && lv[p] > 0.f) M = fmaxf(M, mv[p]);
-#pragma unroll
-  for (int p = 0; p < PMAX; ++p)
-    if (p < parts && lv[p] > 0.f) {
-      const float g = exp2f(mv[p] - M);
-      num = __fmaf_rn(g, ov[p], num);
-      den = __fmaf_rn(g, lv[p], den);
-    }
-  O[(row * H + h) * D + threadIdx.x] = uint16_t(f32_to_bf16_rn(den > 0.f ? num / den : 0.f));
+  const int64_t row = blockIdx.x;
+  const int2 rp = a.row_parts[row];
+  if (rp.y == 1) return;  // written whole
+  const int h = blockIdx.y * HPC + threadIdx.x / TPH, v = threadIdx.x % TPH;
+  if (h >= H) return;
+  float M = -INFINITY;
+#pragma unroll 8
+  for (int p = 0; p < rp.y; ++p) {
+    const int64_t w = int64_t(rp.x + p) * H + h;
+    if (lpart[w] > 0.f) M = fmaxf(M, mpart[w]);
+  }
+  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+  float den = 0.f;
+#pragma unroll 8
+  for (int p = 0; p < rp.y; ++p) {
+    const int64_t w = int64_t(rp.x + p) * H + h;
+    const float l = lpart[w];
+    if (!(l > 0.f)) continue;
+    const float4 o = reinterpret_cast<const float4*>(Opart + w * D)[v];
+    const float g = exp2f(mpart[w] - M);
+    num.x = __fmaf_rn(g, o.x, num.x); num.y = __fmaf_rn(g, o.y, num.y);
+    num.z = __fmaf_rn(g, o.z, num.z); num.w = __fmaf_rn(g, o.w, num.w);
+    den = __fmaf_rn(g, l, den);
+  }
+  const float inv = den > 0.f ? 1.f / den : 0.f;
+  reinterpret_cast<uint2*>(O + (row * H + h) * D)[v] =
+      make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
 }
 
 // ---------------------------------------------------------------------------
@@ -489,25 +547,24 @@ bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStrea
          : TP == 32 ? go(tree_block_scores_kernel<64, 32>) : go(tree_block_scores_kernel<64, 64>);
 }
 
-bool launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s) {
-  const int smem = int(std::max<int64_t>(1, a.capacity / a.B)) * 4;
-  if (cudaFuncSetAttribute(tree_lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-    return false;
+void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s) {
+  const int ranges = int((a.capacity / a.B + kListNT - 1) / kListNT);
   count_launches(1);
-  launch_kernel(true, tree_lists_kernel, unsigned(batch), kListNT, smem, s, a);
-  return true;
+  launch_kernel(true, tree_lists_kernel, unsigned(batch * ranges + 1), kListNT, 0, s, a, int64_t(batch) * a.T, ranges);
 }
 
 void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s) {
   count_launches(1);
-  launch_kernel(true, tree_rows_kernel, unsigned(rows), 256, 0, s, a, idx);
+  launch_kernel(true, tree_rows_kernel, unsigned((rows + 7) / 8), 256, 0, s, a, rows, idx);
 }
 
-void launch_tree_combine(int64_t rows, int H, int d, int parts, const float* Opart, const float* mpart,
+void launch_tree_combine(const TreeArgs& a, int64_t rows, int H, const float* Opart, const float* mpart,
                          const float* lpart, void* O, cudaStream_t s) {
+  const int hpc = 1024 / a.d;
+  const dim3 grid(unsigned(rows), unsigned((H + hpc - 1) / hpc));
   count_launches(1);
-  launch_kernel(true, tree_combine_kernel, unsigned(rows * H), unsigned(d), 0, s, H, d, parts, Opart, mpart, lpart,
-                (uint16_t*)O);
+  launch_kernel(true, a.d == 128 ? tree_combine_kernel<128> : tree_combine_kernel<64>, grid, 256, 0, s, a, H, Opart,
+                mpart, lpart, (uint16_t*)O);
 }
 
 void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,

@@ -67,7 +67,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_token_scores_kernel(const __
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full[C::NS], empty[C::NS], tfull[2], tempty[2], done;
   __shared__ uint32_t tmem_base;
-  __shared__ int slots[4][kTreeMax];  // per epilogue warp: each node's slot of the item's block, or -1
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
@@ -82,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_token_scores_kernel(const __
   const uint32_t tmem = tmem_base;
   griddep_wait();
   griddep_launch();
-  const int total = *a.n_items;
+  const int total = a.counters[0];
   const int g = int(gridDim.x);
   bool dead = false;
 
@@ -148,42 +147,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_token_scores_kernel(const __
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3, r = quad * 32 + lane;
     const uint32_t lane_addr = uint32_t(quad * 32) << 16;
-    int* sl = slots[quad];
     uint32_t it = 0;
     // an item is fetched two ahead, its pairs one ahead
     auto item_of = [&](int tt) { return tt < total ? a.items[tt] : make_int4(0, 0, 0, 0); };
-    auto pair_of = [&](const int4& d, int e) { return e < (d.z & 0xffff) ? a.pairs[d.y + e] : 0xffffffffu; };
+    auto pair_of = [&](const int4& d, int e) { return e < (d.z & 0xffff) ? a.pairs[d.y + e] : 0u; };
     int4 cur = item_of(blockIdx.x), next = item_of(blockIdx.x + g);
     uint32_t p0 = pair_of(cur, lane), p1 = pair_of(cur, lane + 32);
     for (int t = blockIdx.x; t < total && !dead; t += g) {
-      sl[lane] = -1;
-      sl[lane + 32] = -1;
-      __syncwarp();
-      if (p0 != 0xffffffffu) sl[p0 >> 16] = int(p0 & 0xffffu);
-      if (p1 != 0xffffffffu) sl[p1 >> 16] = int(p1 & 0xffffu);
-      __syncwarp();
       const int4 item = cur;
+      const uint32_t q0 = p0, q1 = p1;
       cur = next;
       next = item_of(t + 2 * g);
       p0 = pair_of(cur, lane);
       p1 = pair_of(cur, lane + 32);
-      const int tb = it & 1;
+      const int tb = it & 1, cnt = item.z & 0xffff;
       if (!tw_wait_warp(&tfull[tb], (it >> 1) & 1, dead)) break;
       tc_fence_after();
-      float v[N];
-      tmem_load_f32<N>(tmem + lane_addr + tb * N, v);
+      const bool mine = r < (item.z >> 16);
+      uint32_t* out = a.tkeys + int64_t(item.w >> 3) * a.T * a.m * a.B + 128 * (item.w & 7) + r;
+      // a node's scores are one accumulator column: four pairs' at a time
+      for (int e0 = 0; e0 < cnt; e0 += 4) {
+        uint32_t v[4], pr[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int e = min(e0 + u, cnt - 1);
+          pr[u] = __shfl_sync(kFull, e < 32 ? q0 : q1, e & 31);
+          tmem_ld1(tmem + lane_addr + tb * N + (pr[u] >> 16), v[u]);
+        }
+        tmem_wait_ld();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (mine && e0 + u < cnt)
+            out[(int64_t(pr[u] >> 16) * a.m + (pr[u] & 0xffffu)) * a.B] = score_key(__uint_as_float(v[u]));
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[tb]);
-      const bool mine = r < (item.z >> 16);
-      const int64_t row0 = int64_t(item.w >> 3) * a.T;
-      const int key0 = 128 * (item.w & 7) + r;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int s = i < a.T ? sl[i] : -1;
-        if (s >= 0 && mine) a.tkeys[((row0 + i) * a.m + s) * int64_t(a.B) + key0] = score_key(v[i]);
-      }
-      __syncwarp();  // every lane has read the slots
       ++it;
     }
   }
