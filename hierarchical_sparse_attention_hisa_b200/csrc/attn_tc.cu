@@ -298,24 +298,12 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
   const int Lk = a.Lk, k = a.k, H = a.H;
   const float scale_log2 = a.scale_log2;
   const int ipq = a.items_per_query, tpi = a.tiles_per_item;
-  if (VOTE) griddep_wait();  // the first pass has finished its list
-  const int flagged_n = VOTE && a.redo ? *a.redo : 0;
-  const bool listed = VOTE && a.redo && flagged_n <= a.redo_cap;  // else every item
-  const int n_items = listed ? flagged_n : a.Lq * ipq;
-  if (VOTE && a.redo && flagged_n == 0) return;  // nothing flagged (the whole CTA leaves)
-  // the items of this CTA: wi = w0, w0 + dw, ... below w1
-  const bool given = VOTE && a.items;
-  const int w0 = given ? a.cta_items[blockIdx.x] : int(blockIdx.x);
-  const int w1 = given ? a.cta_items[blockIdx.x + 1] : n_items, dw = given ? 1 : int(gridDim.x);
-  struct Item { int q, t0, tiles, part; };
-  auto item = [&](int wi) -> Item {
-    if (given) {
-      const int4 v = __ldg(a.items + wi);
-      return {v.x, v.y, v.z, v.w};
-    }
-    const int w = listed ? a.redo[1 + wi] : wi, q = w / ipq;
-    return {q, (w - q * ipq) * tpi, tpi, a.O ? -1 : w};
-  };
+  int flagged_n = 0;
+  if (VOTE && a.redo) {
+    griddep_wait();  // the first pass has finished its list
+    flagged_n = *a.redo;
+    if (flagged_n == 0) return;  // nothing flagged (the whole CTA leaves)
+  }
   constexpr int HH = C::HH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -361,6 +349,21 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
   // under a programmatic dependent launch they overlap the previous kernel
   griddep_wait();
   griddep_launch();
+  const bool listed = VOTE && a.redo && flagged_n <= a.redo_cap;  // else every item
+  const int n_items = listed ? flagged_n : a.Lq * ipq;
+  // the items of this CTA: wi = w0, w0 + dw, ... below w1
+  const bool given = VOTE && a.items;
+  const int w0 = given ? a.cta_items[blockIdx.x] : int(blockIdx.x);
+  const int w1 = given ? a.cta_items[blockIdx.x + 1] : n_items, dw = given ? 1 : int(gridDim.x);
+  struct Item { int q, t0, tiles, part; };
+  auto item = [&](int wi) -> Item {
+    if (given) {
+      const int4 v = __ldg(a.items + wi);
+      return {v.x, v.y, v.z, v.w};
+    }
+    const int w = listed ? a.redo[1 + wi] : wi, q = w / ipq;
+    return {q, (w - q * ipq) * tpi, tpi, a.O ? -1 : w};
+  };
 
   if (warp < NPW) {
     // ------------------------------------------------------------ producers

@@ -112,6 +112,12 @@ struct TreeArgs {
   int* cta_items;                  // [kGivenItemCtas + 1]
   int2* row_parts;                 // [rows]
 };
+// Does the selection of a query at position t need token scores?
+HSA_DEV bool needs_scores(int64_t t, int B, int m, int k) {
+  const int64_t nb = t / B + 1;
+  const int64_t n = nb <= m ? t + 1 : int64_t(m - 1) * B + t % B + 1;
+  return n > k;
+}
 void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, const int32_t* n_nodes,
                       const int32_t* parents, int32_t* positions, int32_t* paths, cudaStream_t s);
 // (also appends the drafted rows to the caches and scores every node's tail)

@@ -110,6 +110,10 @@ HSA_DEV void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int x
 HSA_DEV void cp_async16(uint32_t dst_smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
 }
+// The same copy as a part of a 256-byte row that will be read whole: the L2 fetches all of it at once.
+HSA_DEV void cp_async16_row256(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
 // The same copy when `valid`, else 16 zero bytes written without reading `src`.
 HSA_DEV void cp_async16_zfill(uint32_t dst_smem, const void* src, bool valid) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(valid ? 16u : 0u)

@@ -6,9 +6,8 @@
 // so along a node's path position p is row p below ctx and row
 // ctx + path[p - ctx] from there on. Blocks wholly below f = floor(ctx / B)
 // are the same for every node and go through the block-sum cache and the
-// tensor cores (tree_scores.cu); the "tail", positions from f*B on, differs
-// from node to node, is at most B - 1 + T rows long and is scored here. A
-// tail block's score is the sum of its token scores: q . sum k = sum q . k.
+// tensor cores; the "tail", positions from f*B on, differs from node to node
+// and is at most B - 1 + T rows long (tree_scores.cu for both).
 #include <algorithm>
 
 #include "kernels.cuh"
@@ -58,186 +57,6 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(int T, int64_t capacity,
     const int r = e / T, s = e - r * T;
     out[e] = s <= dep[r] ? up[r][dep[r] - s] : -1;
   }
-}
-
-// ---------------------------------------------------------------------------
-// Node block scores. Grid (sequence, part). The first `chunks` parts score 64
-// cached whole blocks each against every node of the sequence:
-// bkeys[row][blk] = key(q . ksum[blk]), fp32 products and sums. The other
-// parts are one node each: append its drafted rows to the caches, score its
-// tail, write the tail's keys and the scores of its whole tail blocks.
-// ---------------------------------------------------------------------------
-constexpr int kBlkChunk = 64;
-constexpr int kNT = 256;
-
-// Does the selection of a node at position t need token scores?
-HSA_DEV bool needs_scores(int64_t t, int B, int m, int k) {
-  const int64_t nb = t / B + 1;
-  const int64_t n = nb <= m ? t + 1 : int64_t(m - 1) * B + t % B + 1;
-  return n > k;
-}
-
-template <int DI>
-HSA_DEV float dot8(const uint4& kv, const float (&q)[8]) {
-  float acc = q[0] * bf16_lo(kv.x);
-  acc = __fmaf_rn(q[1], bf16_hi(kv.x), acc);
-  acc = __fmaf_rn(q[2], bf16_lo(kv.y), acc);
-  acc = __fmaf_rn(q[3], bf16_hi(kv.y), acc);
-  acc = __fmaf_rn(q[4], bf16_lo(kv.z), acc);
-  acc = __fmaf_rn(q[5], bf16_hi(kv.z), acc);
-  acc = __fmaf_rn(q[6], bf16_lo(kv.w), acc);
-  acc = __fmaf_rn(q[7], bf16_hi(kv.w), acc);
-  return acc;
-}
-
-template <int DI>
-__device__ void node_tail(const TreeArgs& a, int64_t b, int i, float* sc) {
-  const int64_t row = b * a.T + i;
-  const int64_t c = a.ctx[b];
-  const int64_t t = a.positions[row];
-  // a plan made for other lengths must not reach outside the sequence's rows
-  const bool ok = c >= 0 && t >= c && t - c <= i && c + i < a.capacity;
-  if (threadIdx.x == 0) a.rowpos[row] = ok ? int32_t(t) : -1;
-  if (!ok) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  {  // the drafted rows, node i in cache row c + i
-    const int64_t at = b * a.capacity + c + i;
-    const int ci = DI / 8, cd = a.d / 8;
-    for (int e = tid; e < ci + 2 * cd; e += kNT) {
-      if (e < ci)
-        reinterpret_cast<uint4*>(a.k_idx_cache + at * DI)[e] = reinterpret_cast<const uint4*>(a.k_idx_new + row * DI)[e];
-      else if (e < ci + cd)
-        reinterpret_cast<uint4*>(a.K_cache + at * a.d)[e - ci] = reinterpret_cast<const uint4*>(a.K_new + row * a.d)[e - ci];
-      else
-        reinterpret_cast<uint4*>(a.V_cache + at * a.d)[e - ci - cd] =
-            reinterpret_cast<const uint4*>(a.V_new + row * a.d)[e - ci - cd];
-    }
-  }
-  const int64_t nb = t / a.B + 1;
-  const int64_t f = c / a.B;
-  const bool tokens = needs_scores(t, a.B, a.m, a.k);
-  const bool blocks = nb > a.m && f < nb - 1;  // whole blocks in the tail
-  if (!tokens && !blocks) return;
-  // tail rows: cached ones from f*B, then the path
-  const int head = int(c - f * a.B), n = head + int(t - c) + 1;
-  constexpr int LPR = DI / 8, RPW = 32 / LPR;
-  const int sub = lane % LPR, rsub = lane / LPR;
-  float q[8];
-  {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.q_new + row * DI) + sub);
-    q[0] = bf16_lo(v.x); q[1] = bf16_hi(v.x); q[2] = bf16_lo(v.y); q[3] = bf16_hi(v.y);
-    q[4] = bf16_lo(v.z); q[5] = bf16_hi(v.z); q[6] = bf16_lo(v.w); q[7] = bf16_hi(v.w);
-  }
-  const uint16_t* cached = a.k_idx_cache + (b * a.capacity + f * a.B) * DI;
-  const int32_t* path = a.paths + row * a.T;
-  uint32_t* keys = a.tailkeys + row * a.tail_ld;
-  constexpr int U = 4;  // rows in flight per lane group
-  for (int r0 = warp * RPW; r0 < n; r0 += (kNT / 32) * RPW * U) {
-    uint4 kv[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * (kNT / 32) * RPW + rsub;
-      kv[u] = make_uint4(0, 0, 0, 0);
-      if (r < head) {
-        kv[u] = *(reinterpret_cast<const uint4*>(cached + int64_t(r) * DI) + sub);
-      } else if (r < n) {
-        const int j = min(max(path[r - head], 0), a.T - 1);
-        kv[u] = __ldg(reinterpret_cast<const uint4*>(a.k_idx_new + (b * a.T + j) * DI) + sub);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int r = r0 + u * (kNT / 32) * RPW + rsub;
-      float acc = dot8<DI>(kv[u], q);
-#pragma unroll
-      for (int o = LPR / 2; o >= 1; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
-      if (sub == 0 && r < n) {
-        sc[r] = acc;
-        keys[r] = score_key(acc);
-      }
-    }
-  }
-  if (!blocks) return;
-  __syncthreads();
-  for (int64_t blk = f + warp; blk < nb - 1; blk += kNT / 32) {
-    float s = 0.f;
-    for (int r = lane; r < a.B; r += 32) s += sc[(blk - f) * a.B + r];
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    if (lane == 0) a.bkeys[row * a.ldb + blk] = score_key(s);
-  }
-}
-
-// 64 blocks x TP nodes, DI summed in shared memory: a thread holds TP/16 nodes
-// x 4 blocks. The operands are read as float4 along the summed axis.
-template <int DI, int TP>
-__device__ void cached_block_scores(const TreeArgs& a, int64_t b, int chunk, float* smem) {
-  const int64_t c = a.ctx[b];
-  if (c < 0 || c >= a.capacity) return;
-  const int64_t f = c / a.B;
-  const int64_t lo = int64_t(chunk) * kBlkChunk, hi = min(f, lo + kBlkChunk);
-  if (lo >= hi) return;
-  if ((c + a.T - 1) / a.B + 1 <= a.m) return;  // every node keeps all its blocks
-  constexpr int LD = DI + 4;
-  float* qs = smem;             // [TP][LD]
-  float* ks = smem + TP * LD;   // [64][LD]
-  const int tid = threadIdx.x;
-  for (int e = tid; e < TP * (DI / 8); e += kNT) {
-    const int n = e / (DI / 8), ch = e % (DI / 8);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (n < a.T) v = __ldg(reinterpret_cast<const uint4*>(a.q_new + (b * a.T + n) * DI) + ch);
-    float4* o = reinterpret_cast<float4*>(qs + n * LD + 8 * ch);
-    o[0] = make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
-    o[1] = make_float4(bf16_lo(v.z), bf16_hi(v.z), bf16_lo(v.w), bf16_hi(v.w));
-  }
-  const float* src = a.ksum_cache + (b * (a.capacity / a.B) + lo) * DI;
-  for (int e = tid; e < kBlkChunk * (DI / 4); e += kNT) {
-    const int n = e / (DI / 4), ch = e % (DI / 4);
-    const float4 v = lo + n < hi ? __ldg(reinterpret_cast<const float4*>(src + n * DI) + ch) : make_float4(0, 0, 0, 0);
-    *reinterpret_cast<float4*>(ks + n * LD + 4 * ch) = v;
-  }
-  __syncthreads();
-  constexpr int NN = TP / 16;
-  const int bg = tid & 15, ng = tid >> 4;  // blocks bg + 16 j, nodes ng + 16 i
-  float acc[NN][4] = {};
-#pragma unroll 4
-  for (int e = 0; e < DI; e += 4) {
-    float4 kv[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(ks + (bg + 16 * j) * LD + e);
-#pragma unroll
-    for (int i = 0; i < NN; ++i) {
-      const float4 qv = *reinterpret_cast<const float4*>(qs + (ng + 16 * i) * LD + e);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][j] = __fmaf_rn(qv.x, kv[j].x, acc[i][j]);
-        acc[i][j] = __fmaf_rn(qv.y, kv[j].y, acc[i][j]);
-        acc[i][j] = __fmaf_rn(qv.z, kv[j].z, acc[i][j]);
-        acc[i][j] = __fmaf_rn(qv.w, kv[j].w, acc[i][j]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NN; ++i) {
-    const int n = ng + 16 * i;
-    if (n >= a.T) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (lo + bg + 16 * j < hi) a.bkeys[(b * a.T + n) * a.ldb + lo + bg + 16 * j] = score_key(acc[i][j]);
-  }
-}
-
-template <int DI, int TP>
-__global__ void __launch_bounds__(kNT) tree_block_scores_kernel(const TreeArgs a, int chunks) {
-  extern __shared__ __align__(16) float smem_f[];
-  griddep_wait();
-  griddep_launch();
-  const int64_t b = blockIdx.x;
-  if (b == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
-  if (int(blockIdx.y) < chunks)
-    cached_block_scores<DI, TP>(a, b, blockIdx.y, smem_f);
-  else
-    node_tail<DI>(a, b, int(blockIdx.y) - chunks, smem_f);
 }
 
 // ---------------------------------------------------------------------------
@@ -324,10 +143,23 @@ __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, i
   const int32_t* blocks = a.blocks + b * a.T * a.m;
   const int entries = a.T * a.m;
   const int end = min(f, lo + kListNT);
-  for (int e = tid; e < entries; e += kListNT) {
-    const int blk = blocks[e];
-    if (blk >= lo && blk < end && pos_s[e / a.m] >= 0) atomicAdd(&hist[blk - lo], 1);
-  }
+  // f(entry, block) for the entries of this range whose nodes need scores, eight loads in flight
+  auto for_entries = [&](auto fn) {
+    for (int e0 = tid; e0 < entries; e0 += 8 * kListNT) {
+      int blk[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int e = e0 + u * kListNT;
+        blk[u] = e < entries ? blocks[e] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int e = e0 + u * kListNT;
+        if (blk[u] >= lo && blk[u] < end && pos_s[e / a.m] >= 0) fn(e, blk[u]);
+      }
+    }
+  };
+  for_entries([&](int, int blk) { atomicAdd(&hist[blk - lo], 1); });
   // tail blocks: their keys, a warp per node, the nodes spread over the ranges
   for (int i = range + warp * ranges; i < a.T; i += kListNT / 32 * ranges) {
     const int t = pos_s[i];
@@ -362,11 +194,10 @@ __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, i
       a.items[s_base[0] + at_i * per + ch] =
           make_int4(int(b * a.capacity) + mine * a.B + 128 * ch, s_base[1] + at_p,
                     cnt | (min(128, a.B - 128 * ch) << 16), int(b << 3) | ch);
-  for (int e = tid; e < entries; e += kListNT) {
-    const int blk = blocks[e], i = e / a.m;
-    if (blk >= lo && blk < end && pos_s[i] >= 0)
-      pairs[atomicAdd(&hist[blk - lo], 1)] = uint32_t(i) << 16 | uint32_t(e - i * a.m);
-  }
+  for_entries([&](int e, int blk) {
+    const int i = e / a.m;
+    pairs[atomicAdd(&hist[blk - lo], 1)] = uint32_t(i) << 16 | uint32_t(e - i * a.m);
+  });
 }
 
 // Kept positions of each node -> rows of its sequence's cache, in place, a warp
@@ -396,41 +227,56 @@ __global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int64_
 
 // O of the rows that were cut (with M the largest part maximum, O = sum_p
 // 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), and of the rows that
-// keep nothing (zero). Grid (row, heads / HPC), a thread per four values.
+// keep nothing (zero). Grid (row, head groups), a thread per four values; the
+// parts come eight at a time, every load of a group issued before any is used.
 template <int D>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int H, const float* __restrict__ Opart,
                                                            const float* __restrict__ mpart,
                                                            const float* __restrict__ lpart, uint16_t* __restrict__ O) {
-  constexpr int TPH = D / 4, HPC = 256 / TPH;  // threads per head, heads per CTA
+  constexpr int TPH = D / 4, HPC = 256 / TPH, U = 8;  // threads per head, heads per CTA at a time
   griddep_wait();
   griddep_launch();
   const int64_t row = blockIdx.x;
   const int2 rp = a.row_parts[row];
   if (rp.y == 1) return;  // written whole
-  const int h = blockIdx.y * HPC + threadIdx.x / TPH, v = threadIdx.x % TPH;
-  if (h >= H) return;
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int p = 0; p < rp.y; ++p) {
-    const int64_t w = int64_t(rp.x + p) * H + h;
-    if (lpart[w] > 0.f) M = fmaxf(M, mpart[w]);
+  const int v = threadIdx.x % TPH;
+  for (int h = blockIdx.y * HPC + threadIdx.x / TPH; h < H; h += gridDim.y * HPC) {
+    float M = -INFINITY, den = 0.f;
+    float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p0 = 0; p0 < rp.y; p0 += U) {
+      float l[U], m[U];
+      float4 o[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = p0 + u < rp.y;
+        const int64_t w = int64_t(rp.x + p0 + u) * H + h;
+        l[u] = in ? lpart[w] : 0.f;
+        m[u] = in ? mpart[w] : -INFINITY;
+        o[u] = in ? reinterpret_cast<const float4*>(Opart + w * D)[v] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (l[u] > 0.f) top = fmaxf(top, m[u]);
+      if (p0 > 0) {
+        const float g = top == -INFINITY ? 1.f : exp2f(M - top);
+        num.x *= g; num.y *= g; num.z *= g; num.w *= g;
+        den *= g;
+      }
+      M = top;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (l[u] > 0.f) {  // an empty part has no weight, and nothing in its O
+          const float g = exp2f(m[u] - M);
+          num.x = __fmaf_rn(g, o[u].x, num.x); num.y = __fmaf_rn(g, o[u].y, num.y);
+          num.z = __fmaf_rn(g, o[u].z, num.z); num.w = __fmaf_rn(g, o[u].w, num.w);
+          den = __fmaf_rn(g, l[u], den);
+        }
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;
+    reinterpret_cast<uint2*>(O + (row * H + h) * D)[v] =
+        make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
   }
-  float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-  float den = 0.f;
-#pragma unroll 8
-  for (int p = 0; p < rp.y; ++p) {
-    const int64_t w = int64_t(rp.x + p) * H + h;
-    const float l = lpart[w];
-    if (!(l > 0.f)) continue;
-    const float4 o = reinterpret_cast<const float4*>(Opart + w * D)[v];
-    const float g = exp2f(mpart[w] - M);
-    num.x = __fmaf_rn(g, o.x, num.x); num.y = __fmaf_rn(g, o.y, num.y);
-    num.z = __fmaf_rn(g, o.z, num.z); num.w = __fmaf_rn(g, o.w, num.w);
-    den = __fmaf_rn(g, l, den);
-  }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  reinterpret_cast<uint2*>(O + (row * H + h) * D)[v] =
-      make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
 }
 
 // ---------------------------------------------------------------------------
@@ -529,24 +375,6 @@ void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, co
                 paths);
 }
 
-bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStream_t s) {
-  const int chunks = int((a.capacity / a.B + kBlkChunk - 1) / kBlkChunk);
-  const dim3 grid(unsigned(batch), unsigned(chunks + a.T));
-  const int TP = a.T <= 16 ? 16 : a.T <= 32 ? 32 : 64;
-  const size_t smem = std::max(size_t(TP + kBlkChunk) * (d_idx + 4) * 4, size_t(a.tail_ld) * 4);
-  auto go = [&](auto kern) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess) return false;
-    count_launches(1);
-    launch_kernel(true, kern, grid, kNT, smem, s, a, chunks);
-    return true;
-  };
-  if (d_idx == 128)
-    return TP == 16 ? go(tree_block_scores_kernel<128, 16>)
-           : TP == 32 ? go(tree_block_scores_kernel<128, 32>) : go(tree_block_scores_kernel<128, 64>);
-  return TP == 16 ? go(tree_block_scores_kernel<64, 16>)
-         : TP == 32 ? go(tree_block_scores_kernel<64, 32>) : go(tree_block_scores_kernel<64, 64>);
-}
-
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s) {
   const int ranges = int((a.capacity / a.B + kListNT - 1) / kListNT);
   count_launches(1);
@@ -560,8 +388,9 @@ void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_
 
 void launch_tree_combine(const TreeArgs& a, int64_t rows, int H, const float* Opart, const float* mpart,
                          const float* lpart, void* O, cudaStream_t s) {
-  const int hpc = 1024 / a.d;
-  const dim3 grid(unsigned(rows), unsigned((H + hpc - 1) / hpc));
+  // a CTA per head group, fewer when the rows alone make a large grid (most of a large call's rows were written whole)
+  const int64_t groups = std::min<int64_t>((H * a.d + 1023) / 1024, std::max<int64_t>(1, 16384 / rows));
+  const dim3 grid{unsigned(rows), unsigned(groups)};
   count_launches(1);
   launch_kernel(true, a.d == 128 ? tree_combine_kernel<128> : tree_combine_kernel<64>, grid, 256, 0, s, a, H, Opart,
                 mpart, lpart, (uint16_t*)O);

@@ -1,19 +1,11 @@
-// Token scores of a drafted tree inside the kept cached blocks, on tcgen05:
-//   S^T[key][node] = k_idx[row0 + key] . q_idx[node]
-// for every (node, slot) pair that kept a block. An item is up to 128 rows of
-// one block with the nodes that kept it. The keys are the MMA's M dimension
-// and all of a sequence's nodes its N (16, 32 or 64 columns), so a block is
-// read once whatever number of nodes kept it, nothing is gathered, and an
-// accumulator column is one node's scores of 128 consecutive keys: the 128
-// epilogue threads (TMEM lane = key) write it as 512 contiguous bytes.
-//
-// The keys are what bounds it: 2 * d_idx bytes a row from HBM (or L2) against
-// 2 * N * d_idx FLOP, far below the tensor peak at N <= 64.
-//
-// Warp roles of the persistent kernel: warp 0 TMA producer (key rows and the
-// sequence's query rows of an item), warp 1 MMA issuer (+ TMEM owner), warps
-// 2-5 epilogue. The accumulator is two deep, so an item's epilogue overlaps
-// the next one's MMAs. Every wait is bounded.
+// Scores of a drafted tree's nodes, on tcgen05 where nodes share what they
+// score. In both kernels the scored rows are the MMA's M dimension and all of a
+// sequence's nodes its N (16, 32 or 64 columns), so a row is read once whatever
+// number of nodes it is scored for, and an accumulator column is one node's
+// scores of 128 consecutive rows: 128 epilogue threads (TMEM lane = row) write
+// it as 512 contiguous bytes. Every wait is bounded.
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "tc.cuh"
 
@@ -45,6 +37,261 @@ HSA_DEV bool tw_wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
   return ok;
 }
 
+// ---------------------------------------------------------------------------
+// Block scores, grid (sequence, 128 cached whole blocks):
+//   bkeys[row][blk] = key(q . ksum[blk]),  ksum = hi + mid + lo in bf16,
+// three MMAs per 16 summed values (as the prefill's block scores: exact for
+// sums of at most 24 significant bits). A CTA reads its fp32 sums once (HBM),
+// splits them in registers and writes the planes straight into the swizzled
+// layout the MMA reads. On CUDA cores the same tile is bound by shared memory
+// (2.4 us per SM at 16 nodes, FMAs at 64).
+//
+// Tails, a launch of its own with four warps per node: append the node's
+// drafted rows to the caches and score its tail, the rows of its path from f*B
+// on. A tail block's score is the sum of its token scores: q . sum k =
+// sum q . k.
+//
+// The two do not depend on one another, and the tails' CTAs are small, the
+// blocks' (113 KB at d_idx = 128) two to an SM: as parts of one launch they ran
+// as two waves (17 us for 32 x 16 nodes at 128K), as two they share the SMs.
+// ---------------------------------------------------------------------------
+constexpr int kBlkTile = 128;
+constexpr int kNT = 256, kNodeNT = 128, kNodesPerCta = kNT / kNodeNT;
+
+HSA_DEV float dot8(const uint4& kv, const float (&q)[8]) {
+  float acc = q[0] * bf16_lo(kv.x);
+  acc = __fmaf_rn(q[1], bf16_hi(kv.x), acc);
+  acc = __fmaf_rn(q[2], bf16_lo(kv.y), acc);
+  acc = __fmaf_rn(q[3], bf16_hi(kv.y), acc);
+  acc = __fmaf_rn(q[4], bf16_lo(kv.z), acc);
+  acc = __fmaf_rn(q[5], bf16_hi(kv.z), acc);
+  acc = __fmaf_rn(q[6], bf16_lo(kv.w), acc);
+  acc = __fmaf_rn(q[7], bf16_hi(kv.w), acc);
+  return acc;
+}
+
+// tid: 0 .. kNodeNT-1 within the node's warps; bar: their named barrier; sc: tail_ld floats
+template <int DI>
+__device__ void node_tail(const TreeArgs& a, int64_t b, int i, int tid, int bar, float* sc) {
+  const int64_t row = b * a.T + i;
+  const int64_t c = a.ctx[b];
+  const int64_t t = a.positions[row];
+  // a plan made for other lengths must not reach outside the sequence's rows
+  const bool ok = c >= 0 && t >= c && t - c <= i && c + i < a.capacity;
+  if (tid == 0) a.rowpos[row] = ok ? int32_t(t) : -1;
+  if (!ok) return;
+  const int lane = tid & 31, warp = tid >> 5;
+  {  // the drafted rows, node i in cache row c + i
+    const int64_t at = b * a.capacity + c + i;
+    const int ci = DI / 8, cd = a.d / 8;
+    for (int e = tid; e < ci + 2 * cd; e += kNodeNT) {
+      if (e < ci)
+        reinterpret_cast<uint4*>(a.k_idx_cache + at * DI)[e] = reinterpret_cast<const uint4*>(a.k_idx_new + row * DI)[e];
+      else if (e < ci + cd)
+        reinterpret_cast<uint4*>(a.K_cache + at * a.d)[e - ci] = reinterpret_cast<const uint4*>(a.K_new + row * a.d)[e - ci];
+      else
+        reinterpret_cast<uint4*>(a.V_cache + at * a.d)[e - ci - cd] =
+            reinterpret_cast<const uint4*>(a.V_new + row * a.d)[e - ci - cd];
+    }
+  }
+  const int64_t nb = t / a.B + 1;
+  const int64_t f = c / a.B;
+  const bool tokens = needs_scores(t, a.B, a.m, a.k);
+  const bool blocks = nb > a.m && f < nb - 1;  // whole blocks in the tail
+  if (!tokens && !blocks) return;
+  // tail rows: cached ones from f*B, then the path
+  const int head = int(c - f * a.B), n = head + int(t - c) + 1;
+  constexpr int LPR = DI / 8, RPW = 32 / LPR, NW = kNodeNT / 32;
+  const int sub = lane % LPR, rsub = lane / LPR;
+  float q[8];
+  {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.q_new + row * DI) + sub);
+    q[0] = bf16_lo(v.x); q[1] = bf16_hi(v.x); q[2] = bf16_lo(v.y); q[3] = bf16_hi(v.y);
+    q[4] = bf16_lo(v.z); q[5] = bf16_hi(v.z); q[6] = bf16_lo(v.w); q[7] = bf16_hi(v.w);
+  }
+  const uint16_t* cached = a.k_idx_cache + (b * a.capacity + f * a.B) * DI;
+  const int32_t* path = a.paths + row * a.T;
+  uint32_t* keys = a.tailkeys + row * a.tail_ld;
+  constexpr int U = 8;  // rows in flight per lane group
+  for (int r0 = warp * RPW; r0 < n; r0 += NW * RPW * U) {
+    uint4 kv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * NW * RPW + rsub;
+      kv[u] = make_uint4(0, 0, 0, 0);
+      if (r < head) {
+        kv[u] = *(reinterpret_cast<const uint4*>(cached + int64_t(r) * DI) + sub);
+      } else if (r < n) {
+        const int j = min(max(path[r - head], 0), a.T - 1);
+        kv[u] = __ldg(reinterpret_cast<const uint4*>(a.k_idx_new + (b * a.T + j) * DI) + sub);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * NW * RPW + rsub;
+      float acc = dot8(kv[u], q);
+#pragma unroll
+      for (int o = LPR / 2; o >= 1; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
+      if (sub == 0 && r < n) {
+        sc[r] = acc;
+        keys[r] = score_key(acc);
+      }
+    }
+  }
+  if (!blocks) return;
+  bar_sync(bar, kNodeNT);
+  for (int64_t blk = f + warp; blk < nb - 1; blk += NW) {
+    float s = 0.f;
+    for (int r = lane; r < a.B; r += 32) s += sc[(blk - f) * a.B + r];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+    if (lane == 0) a.bkeys[row * a.ldb + blk] = score_key(s);
+  }
+}
+
+template <int DI, int N>
+struct BS {
+  static constexpr int PLANE = kBlkTile * DI * 2;  // one bf16 plane of the sums
+  static constexpr int OFF_Q = 3 * PLANE;
+  static constexpr int SMEM = OFF_Q + N * DI * 2 + 1024;
+  static constexpr int TMEM_COLS = N < 32 ? 32 : N;
+};
+
+template <int DI, int N>
+__device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint8_t* sm, uint64_t* bar,
+                                    uint32_t* tmem_base) {
+  using C = BS<DI, N>;
+  constexpr int CPR = DI / 8;  // eight-value chunks per row
+  const int64_t c = a.ctx[b];
+  if (c < 0 || c >= a.capacity) return;
+  const int64_t f = c / a.B;
+  const int64_t lo = int64_t(tile) * kBlkTile;
+  const int n = int(min(int64_t(kBlkTile), f - lo));
+  if (n <= 0) return;
+  if ((c + a.T - 1) / a.B + 1 <= a.m) return;  // every node keeps all its blocks
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const float4* src = reinterpret_cast<const float4*>(a.ksum_cache + (b * (a.capacity / a.B) + lo) * DI);
+  constexpr int PER = kBlkTile * CPR / kNT;
+  float4 x[PER][2];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int e = tid + u * kNT;  // (row, chunk) = (e / CPR, e % CPR)
+    x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (e / CPR < n) {
+      x[u][0] = __ldg(src + 2 * e);
+      x[u][1] = __ldg(src + 2 * e + 1);
+    }
+  }
+  if (warp == 0) { tmem_alloc(tmem_base, C::TMEM_COLS); tmem_relinquish(); }
+  if (tid == 0) { mbar_init(bar, 1); fence_barrier_init(); }
+  for (int e = tid; e < a.T * CPR; e += kNT) {  // (columns past the nodes hold anything: nobody reads them)
+    const int r = e / CPR, ch = e % CPR;
+    *reinterpret_cast<uint4*>(sm + C::OFF_Q + (ch >> 3) * (N * 128) + swz_offset(r, ch & 7, 128)) =
+        __ldg(reinterpret_cast<const uint4*>(a.q_new + b * a.T * DI) + e);
+  }
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int e = tid + u * kNT, r = e / CPR, ch = e % CPR;
+    const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+    uint32_t w[3][4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      float r0 = v[2 * h], r1 = v[2 * h + 1];
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        w[pl][h] = cvt_bf16x2(r0, r1);
+        r0 -= bf16_lo(w[pl][h]);
+        r1 -= bf16_hi(w[pl][h]);
+      }
+    }
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl)
+      *reinterpret_cast<uint4*>(sm + pl * C::PLANE + (ch >> 3) * (kBlkTile * 128) + swz_offset(r, ch & 7, 128)) =
+          make_uint4(w[pl][0], w[pl][1], w[pl][2], w[pl][3]);
+  }
+  fence_proxy_async_smem();  // written by the generic proxy, read by the MMA
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_base;
+  bool dead = false;
+  if (tid == 0) {
+    constexpr uint32_t idesc = idesc_bf16(128, N, false, false);
+    const uint32_t a_s = smem_u32(sm), b_s = a_s + C::OFF_Q;
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl)
+#pragma unroll
+      for (int ks = 0; ks < DI / 16; ++ks) {
+        const uint64_t da = smem_desc(a_s + pl * C::PLANE + (ks / 4) * kBlkTile * 128 + (ks % 4) * 32, 16, 1024, kSw128);
+        const uint64_t db = smem_desc(b_s + (ks / 4) * N * 128 + (ks % 4) * 32, 16, 1024, kSw128);
+        mma_bf16(tmem, da, db, idesc, pl + ks > 0);
+      }
+    mma_commit(bar);
+  }
+  __syncwarp();
+  // warps 0-3 take the first half of the columns, warps 4-7 the second
+  const bool ok = tw_wait_warp(bar, 0, dead);
+  if (ok) {
+    tc_fence_after();
+    constexpr int NH = N / 2;
+    const int r = (warp & 3) * 32 + lane, n0 = (warp >> 2) * NH;
+    float v[NH];
+    tmem_load_f32<NH>(tmem + (uint32_t((warp & 3) * 32) << 16) + n0, v);
+    uint32_t* out = a.bkeys + b * a.T * a.ldb + lo + r;
+    if (r < n) {
+#pragma unroll
+      for (int i = 0; i < NH; ++i)
+        if (n0 + i < a.T) out[int64_t(n0 + i) * a.ldb] = score_key(v[i]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int DI>
+__global__ void __launch_bounds__(kNT) tree_tails_kernel(const TreeArgs a) {
+  extern __shared__ __align__(16) float tail_smem[];
+  griddep_wait();
+  griddep_launch();
+  const int64_t b = blockIdx.x;
+  if (b == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
+  const int half = threadIdx.x / kNodeNT, i = int(blockIdx.y) * kNodesPerCta + half;
+  if (i < a.T) node_tail<DI>(a, b, i, threadIdx.x % kNodeNT, 1 + half, tail_smem + half * a.tail_ld);
+}
+
+// Launched dependent on the tails and run beside them: its CTAs start once
+// every tail CTA has passed its own wait for the work before it, which is all
+// that the scores depend on. The wait at the end makes the kernels after this
+// one, which wait for it alone, wait for the tails too.
+template <int DI, int N>
+__global__ void __launch_bounds__(kNT) tree_block_scores_kernel(const TreeArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ uint32_t tmem_base;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  griddep_launch();
+  cached_block_scores<DI, N>(a, blockIdx.x, blockIdx.y, sm, &bar, &tmem_base);
+  griddep_wait();
+}
+
+// ---------------------------------------------------------------------------
+// Token scores inside the kept cached blocks:
+//   S^T[key][node] = k_idx[row0 + key] . q_idx[node]
+// for every (node, slot) pair that kept a block. An item is up to 128 rows of
+// one block with the nodes that kept it.
+//
+// The keys are what bounds it: 2 * d_idx bytes a row from HBM (or L2) against
+// 2 * N * d_idx FLOP, far below the tensor peak at N <= 64.
+//
+// Warp roles of the persistent kernel: warp 0 TMA producer (key rows and the
+// sequence's query rows of an item), warp 1 MMA issuer (+ TMEM owner), warps
+// 2-5 epilogue. The accumulator is two deep, so an item's epilogue overlaps
+// the next one's MMAs.
+// ---------------------------------------------------------------------------
 template <int DK, int N>
 struct TS {
   static constexpr int KB = DK / 64;              // 128-byte column blocks per row
@@ -205,7 +452,28 @@ bool launch_n(const CUtensorMap& km, const CUtensorMap& qm, const TreeArgs& a, i
   return true;
 }
 
+template <int DI, int N>
+bool launch_bs(const TreeArgs& a, int batch, cudaStream_t s) {
+  const int smem_t = kNodesPerCta * a.tail_ld * 4, smem_b = BS<DI, N>::SMEM;
+  const int tiles = int((a.capacity / a.B + kBlkTile - 1) / kBlkTile);
+  auto blocks = tree_block_scores_kernel<DI, N>;
+  if (cudaFuncSetAttribute(blocks, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_b) != cudaSuccess) return false;
+  count_launches(2);
+  launch_kernel(true, tree_tails_kernel<DI>, dim3(unsigned(batch), unsigned((a.T + kNodesPerCta - 1) / kNodesPerCta)),
+                kNT, size_t(smem_t), s, a);
+  launch_kernel(true, blocks, dim3(unsigned(batch), unsigned(tiles)), kNT, size_t(smem_b), s, a);
+  return true;
+}
+
 }  // namespace
+
+bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStream_t s) {
+  if (d_idx == 128)
+    return a.T <= 16 ? launch_bs<128, 16>(a, batch, s)
+           : a.T <= 32 ? launch_bs<128, 32>(a, batch, s) : launch_bs<128, 64>(a, batch, s);
+  return a.T <= 16 ? launch_bs<64, 16>(a, batch, s)
+         : a.T <= 32 ? launch_bs<64, 32>(a, batch, s) : launch_bs<64, 64>(a, batch, s);
+}
 
 bool launch_tree_token_scores(const TreeArgs& a, int batch, int d_idx, int64_t max_items, cudaStream_t s) {
   const int box_rows = a.B < 128 ? a.B : 128;
