@@ -197,13 +197,15 @@ int hsa_device_status(int reset) {
   const int a = hsa::attn_wait_flag(reset != 0);
   const int b = hsa::score_wait_flag(reset != 0);
   const int c = hsa::tree_wait_flag(reset != 0);
-  if (a < 0 || b < 0 || c < 0) return HSA_ERR_CUDA;
-  return a || b || c ? HSA_ERR_TIMEOUT : HSA_OK;
+  const int d = hsa::tree_attn_wait_flag(reset != 0);
+  if (a < 0 || b < 0 || c < 0 || d < 0) return HSA_ERR_CUDA;
+  return a || b || c || d ? HSA_ERR_TIMEOUT : HSA_OK;
 }
 
 int hsa_debug_inject_lost_arrival(int on) {
   if (int e = check_device()) return e;
-  if (!hsa::attn_set_inject(on != 0) || !hsa::score_set_inject(on != 0) || !hsa::tree_set_inject(on != 0))
+  if (!hsa::attn_set_inject(on != 0) || !hsa::score_set_inject(on != 0) || !hsa::tree_set_inject(on != 0) ||
+      !hsa::tree_attn_set_inject(on != 0))
     return HSA_ERR_CUDA;
   return HSA_OK;
 }
@@ -444,9 +446,9 @@ namespace {
 //   keys [rows][tail_ld] u32, kept blocks [rows][m] i32, pairs [rows][m] u32,
 //   items [max_items] int4, token-score keys [rows][m*B] u32, indices [rows][k]
 //   i32 (unless the caller takes them), the attention's items, their CTAs' first
-//   ones and the rows' parts, and the parts: O f32, maxima and row sums f32.
+//   ones, the rows' parts and flags, and the parts: O f32, maxima and row sums f32.
 struct TreeWs {
-  size_t counters, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, aitems, cta, rparts, opart, mpart, lpart,
+  size_t counters, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, aitems, cta, rparts, flags, opart, mpart, lpart,
       total;
   int64_t rows, ldb, max_items;
   int tail_ld;
@@ -470,10 +472,11 @@ TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) 
   w.tkeys = take(rows * p->m * p->B * 4);
   w.idx = take(rows * p->k * 4);
   // a CTA's list has at most two rows that it shares with its neighbours
-  const size_t parts = 2 * hsa::kGivenItemCtas;
-  w.aitems = take((rows + hsa::kGivenItemCtas) * 16);
-  w.cta = take((hsa::kGivenItemCtas + 1) * 4);
+  const size_t parts = 2 * hsa::kTreeAttnCtas;
+  w.aitems = take((rows + hsa::kTreeAttnCtas) * 16);
+  w.cta = take((hsa::kTreeAttnCtas + 1) * 4);
   w.rparts = take(rows * 8);
+  w.flags = take(rows * 4);
   w.opart = take(parts * p->H * p->d * 4);
   w.mpart = take(parts * p->H * 4);
   w.lpart = take(parts * p->H * 4);
@@ -555,6 +558,7 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   a.attn_items = reinterpret_cast<int4*>(ws + w.aitems);
   a.cta_items = reinterpret_cast<int*>(ws + w.cta);
   a.row_parts = reinterpret_cast<int2*>(ws + w.rparts);
+  a.flags = reinterpret_cast<int*>(ws + w.flags);
   // A node's row of the selections is at the node's own position; a row that
   // takes no part has position -1.
   hsa::RowMap rm{w.rows, capacity, a.rowpos, capacity};
@@ -571,10 +575,8 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   float* opart = reinterpret_cast<float*>(ws + w.opart);
   float* mpart = reinterpret_cast<float*>(ws + w.mpart);
   float* lpart = reinterpret_cast<float*>(ws + w.lpart);
-  if (!hsa::launch_sparse_attn_tc_items(w.rows, T, Q_new, K_cache, V_cache, idx, capacity, p->k, p->H, p->d,
-                                        softmax_scale(p), a.attn_items, a.cta_items, O, opart, mpart, lpart, stream))
-    return HSA_ERR_CUDA;
-  hsa::launch_tree_combine(a, w.rows, p->H, opart, mpart, lpart, O, stream);
+  if (!hsa::launch_tree_attn(a, Q_new, idx, p->H, softmax_scale(p), O, opart, mpart, lpart, stream)) return HSA_ERR_CUDA;
+  hsa::launch_tree_combine(a, w.rows, Q_new, idx, p->H, softmax_scale(p), opart, mpart, lpart, O, stream);
   return launch_status();
 }
 

@@ -106,8 +106,7 @@ struct Bars {
 }  // namespace
 
 // Work description of one launch. Query q's kept indices are idx[q][0..k);
-// its K/V rows start at row (q / q_per_seq) * kv_stride (stride 0: one K/V
-// shared by all queries).
+// its K/V rows start at row q * kv_stride (0: one K/V shared by all queries).
 // The launch covers heads [h0, h0 + nh) of the H heads of each Q / O row.
 // Each query is cut into items_per_query parts of tiles_per_item 128-key
 // tiles; with one part per query the kernel writes normalised O, otherwise
@@ -116,24 +115,18 @@ struct Bars {
 // first pass flagged, listed in redo[1 .. redo_cap] (an item once per softmax
 // warpgroup that flagged it); the second pass takes them in that order, or
 // every item when the count is above redo_cap or there is no list (a launch
-// of the second pass alone, as the decode step makes). With `items` given (a
-// second pass alone), CTA c takes items[cta_items[c] .. cta_items[c + 1]) in
-// their place, each (query, first tile, tiles, part): part < 0 writes O, else
-// part w of the three part arrays.
+// of the second pass alone, as the decode step makes).
 struct AttnArgs {
   const uint16_t* Q;
   const int32_t* idx;
   int Lq, Lk, k, H, h0, nh;
   float scale_log2;
   int64_t kv_stride;
-  int q_per_seq;
   int items_per_query, tiles_per_item;
   uint16_t* O;
   float *Opart, *mpart, *lpart;  // [items][H][d], [items][H], [items][H]
   int* redo;                     // [1 + redo_cap]
   int redo_cap;
-  const int4* items;
-  const int* cta_items;          // [gridDim.x + 1]
 };
 
 namespace {
@@ -298,12 +291,13 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
   const int Lk = a.Lk, k = a.k, H = a.H;
   const float scale_log2 = a.scale_log2;
   const int ipq = a.items_per_query, tpi = a.tiles_per_item;
-  int flagged_n = 0;
-  if (VOTE && a.redo) {
-    griddep_wait();  // the first pass has finished its list
-    flagged_n = *a.redo;
-    if (flagged_n == 0) return;  // nothing flagged (the whole CTA leaves)
-  }
+  if (VOTE) griddep_wait();  // the first pass has finished its list
+  const int flagged_n = VOTE && a.redo ? *a.redo : 0;
+  const bool listed = VOTE && a.redo && flagged_n <= a.redo_cap;  // else every item
+  const int n_items = listed ? flagged_n : a.Lq * ipq;
+  if (VOTE && a.redo && flagged_n == 0) return;  // nothing flagged (the whole CTA leaves)
+  // the w-th item of this pass
+  auto item = [&](int w) { return listed ? a.redo[1 + w] : w; };
   constexpr int HH = C::HH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -349,21 +343,6 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
   // under a programmatic dependent launch they overlap the previous kernel
   griddep_wait();
   griddep_launch();
-  const bool listed = VOTE && a.redo && flagged_n <= a.redo_cap;  // else every item
-  const int n_items = listed ? flagged_n : a.Lq * ipq;
-  // the items of this CTA: wi = w0, w0 + dw, ... below w1
-  const bool given = VOTE && a.items;
-  const int w0 = given ? a.cta_items[blockIdx.x] : int(blockIdx.x);
-  const int w1 = given ? a.cta_items[blockIdx.x + 1] : n_items, dw = given ? 1 : int(gridDim.x);
-  struct Item { int q, t0, tiles, part; };
-  auto item = [&](int wi) -> Item {
-    if (given) {
-      const int4 v = __ldg(a.items + wi);
-      return {v.x, v.y, v.z, v.w};
-    }
-    const int w = listed ? a.redo[1 + wi] : wi, q = w / ipq;
-    return {q, (w - q * ipq) * tpi, tpi, a.O ? -1 : w};
-  };
 
   if (warp < NPW) {
     // ------------------------------------------------------------ producers
@@ -375,21 +354,19 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
     // 128B-swizzled K-major tile, before the swizzle of the chunk
     const uint32_t dbase = (cpk >> 3) * (TILE * 128) + (32 * warp + rsub) * 128;
     const TailScan ts{(k & 3) == 0 && k >= 128, ((k & 3) == 0 && k >= 128) ? k - 128 : 0};
-    int4 pre = w0 < w1 ? ts.window(idx, item(w0).q, k) : make_int4(-1, -1, -1, -1);
+    int4 pre = int(blockIdx.x) < n_items ? ts.window(idx, item(blockIdx.x) / ipq, k) : make_int4(-1, -1, -1, -1);
     const bool inject = *(volatile int*)&g_attn_inject != 0;
     uint32_t g = 0, qn = 0;
-    for (int wi = w0; wi < w1 && !dead; wi += dw, ++qn) {
-      const Item it = item(wi);
-      const int q = it.q;
+    for (int wi = blockIdx.x; wi < n_items && !dead; wi += gridDim.x, ++qn) {
+      const int w = item(wi), q = w / ipq, part = w - q * ipq;
       const int32_t* row = idx + int64_t(q) * k;
-      const int64_t kv0 = int64_t(q / a.q_per_seq) * a.kv_stride * DH;
-      const uint4* Kq = reinterpret_cast<const uint4*>(K + kv0);
-      const uint4* Vq = reinterpret_cast<const uint4*>(V + kv0);
+      const uint4* Kq = reinterpret_cast<const uint4*>(K + int64_t(q) * a.kv_stride * DH);
+      const uint4* Vq = reinterpret_cast<const uint4*>(V + int64_t(q) * a.kv_stride * DH);
       const int4 win = pre;
-      if (wi + dw < w1) pre = ts.window(idx, item(wi + dw).q, k);
+      if (wi + int(gridDim.x) < n_items) pre = ts.window(idx, item(wi + gridDim.x) / ipq, k);
       const int last = ts.last_valid(win, row, k, Lk);
-      const int t0 = it.t0;                                       // this item's tiles
-      const int nt = max(0, min((last + TILE) / TILE, t0 + it.tiles) - t0);
+      const int t0 = part * tpi;                                  // this item's tiles
+      const int nt = max(0, min((last + TILE) / TILE, t0 + tpi) - t0);
       const int qb = qn & 1;
       // warp 0: this query's HP head rows of Q (rows past its nh heads: zeros)
       // and its tile count; the other producers go straight on to its tiles
@@ -445,7 +422,7 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_bf16(128, HP, false, false);
       uint32_t g = 0, qn = 0;
-      for (int wi = w0; wi < w1 && !dead; wi += dw, ++qn) {
+      for (int wi = blockIdx.x; wi < n_items && !dead; wi += gridDim.x, ++qn) {
         const int qb = qn & 1;
         if (!wait_bar(&bars.qfull[qb], (qn >> 1) & 1, dead)) break;
         const int nt = qinfo[qb][1];
@@ -484,7 +461,7 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
     if (lane == 0) {
       constexpr uint32_t id_o = idesc_bf16(128, HP, true, true);
       uint32_t g = 0, qn = 0, oq = 0;
-      for (int wi = w0; wi < w1 && !dead; wi += dw, ++qn) {
+      for (int wi = blockIdx.x; wi < n_items && !dead; wi += gridDim.x, ++qn) {
         const int qb = qn & 1;
         if (!wait_bar(&bars.qfull[qb], (qn >> 1) & 1, dead)) break;
         const int nt = qinfo[qb][1];
@@ -537,10 +514,8 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
     const int h0 = wg * HH;                 // first head of this warpgroup
     const uint32_t lane_addr = uint32_t(quad * 32) << 16;
     uint32_t g = 0, qn = 0, oq = 0;
-    for (int wi = w0; wi < w1; wi += dw, ++qn) {
-      const Item it = item(wi);
-      const int q = it.q;
-      const int64_t w = it.part;  // the part this item writes, if any
+    for (int wi = blockIdx.x; wi < n_items; wi += gridDim.x, ++qn) {
+      const int w = item(wi), q = w / ipq;
       const int qb = qn & 1;
       const bool okq = wait_all(&bars.qfull[qb], (qn >> 1) & 1, dead);
       if (wg_or(bar_id, !okq || dead)) { dead = true; break; }
@@ -548,15 +523,15 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.qempty[qb]);
       // this query's rows of O (head a.h0 + h0 + h of the launch's heads)
-      uint16_t* orow = w < 0 ? a.O + (int64_t(q) * H + a.h0) * DH : nullptr;
+      uint16_t* orow = a.O ? a.O + (int64_t(q) * H + a.h0) * DH : nullptr;
       if (nt == 0) {
         if (orow) {
 #pragma unroll
           for (int h = 0; h < HH; ++h)
             if (h0 + h < nh && r < DH) orow[(h0 + h) * DH + r] = 0;
         } else if (r < HH && h0 + r < nh) {  // an empty part: no weight in the combination
-          a.mpart[w * H + a.h0 + h0 + r] = -INFINITY;
-          a.lpart[w * H + a.h0 + h0 + r] = 0.f;
+          a.mpart[int64_t(w) * H + a.h0 + h0 + r] = -INFINITY;
+          a.lpart[int64_t(w) * H + a.h0 + h0 + r] = 0.f;
         }
         continue;
       }
@@ -715,7 +690,7 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
       const bool flagged = wg_or(bar_id, !VOTE && flag);
       if (flagged && r == 0) {
         const int at = atomicAdd(a.redo, 1);
-        if (at < a.redo_cap) a.redo[1 + at] = wi;
+        if (at < a.redo_cap) a.redo[1 + at] = w;
       }
       if (r < HH) {
         const float l = red[0][h0 + r] + red[1][h0 + r] + red[2][h0 + r] + red[3][h0 + r];
@@ -735,13 +710,13 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
           }
         } else {
           // one part of a split query: unnormalised O^T, running maximum, row sum
-          float* op = a.Opart + (w * H + a.h0) * DH;
+          float* op = a.Opart + (int64_t(w) * H + a.h0) * DH;
 #pragma unroll
           for (int h = 0; h < HH; ++h)
             if (h0 + h < nh && r < DH) op[(h0 + h) * DH + r] = ov[h];
           if (r < HH && h0 + r < nh) {
-            a.mpart[w * H + a.h0 + h0 + r] = mh[h0 + r];
-            a.lpart[w * H + a.h0 + h0 + r] = lsum[h0 + r];
+            a.mpart[int64_t(w) * H + a.h0 + h0 + r] = mh[h0 + r];
+            a.lpart[int64_t(w) * H + a.h0 + h0 + r] = lsum[h0 + r];
           }
         }
       }
@@ -774,7 +749,7 @@ bool launch_hp(const AttnArgs& a, const void* K, const void* V, cudaStream_t s, 
       cudaFuncSetAttribute(second, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
     return false;
   const int64_t items = int64_t(a.Lq) * a.items_per_query;
-  const int grid = a.items ? kGivenItemCtas : int(items < num_sms() ? items : num_sms());
+  const int grid = int(items < num_sms() ? items : num_sms());
   const auto Kp = static_cast<const uint16_t*>(K);
   const auto Vp = static_cast<const uint16_t*>(V);
   if (!two_pass) {
@@ -834,7 +809,6 @@ bool launch_sparse_attn_tc(int64_t Lq, const void* Q, const void* K, const void*
   a.idx = idx; a.Lq = int(Lq); a.Lk = int(Lk); a.k = k; a.H = H;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.kv_stride = 0;
-  a.q_per_seq = 1;
   a.items_per_query = 1;
   a.tiles_per_item = (k + TILE - 1) / TILE;
   a.O = static_cast<uint16_t*>(O);
@@ -850,31 +824,12 @@ bool launch_sparse_attn_tc_split(int batch, const void* Q, const void* Kc, const
   a.idx = idx; a.Lq = batch; a.Lk = int(capacity); a.k = k; a.H = H;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.kv_stride = capacity;
-  a.q_per_seq = 1;
   a.items_per_query = parts;
   a.tiles_per_item = ((k + TILE - 1) / TILE + parts - 1) / parts;
   a.O = nullptr;
   a.Opart = Opart; a.mpart = mpart; a.lpart = lpart;
   // parts of at most a few tiles: the per-tile vote costs less there than a second launch
   return launch_args(a, d, Kc, Vc, s, pdl, false);
-}
-
-bool launch_sparse_attn_tc_items(int64_t rows, int rows_per_seq, const void* Q, const void* Kc, const void* Vc,
-                                 const int32_t* idx, int64_t capacity, int k, int H, int d, float scale,
-                                 const int4* items, const int* cta_items, void* O, float* Opart, float* mpart,
-                                 float* lpart, cudaStream_t s) {
-  if (rows == 0) return true;
-  AttnArgs a{};
-  a.Q = static_cast<const uint16_t*>(Q);
-  a.idx = idx; a.Lq = int(rows); a.Lk = int(capacity); a.k = k; a.H = H;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.kv_stride = capacity;
-  a.q_per_seq = rows_per_seq;
-  a.items_per_query = a.tiles_per_item = 1;
-  a.O = static_cast<uint16_t*>(O);
-  a.Opart = Opart; a.mpart = mpart; a.lpart = lpart;
-  a.items = items; a.cta_items = cta_items;
-  return launch_args(a, d, Kc, Vc, s, true, false);
 }
 
 // Host side: whether a bounded wait of this kernel gave up on the current

@@ -77,14 +77,6 @@ void launch_decode_combine(int batch, int64_t capacity, int32_t* ctx, int H, int
 bool launch_sparse_attn_tc_split(int batch, const void* Q, const void* Kc, const void* Vc, const int32_t* idx,
                                  int64_t capacity, int k, int H, int d, float scale, int parts, float* Opart,
                                  float* mpart, float* lpart, cudaStream_t s, bool pdl = false);
-// Attention of `rows` queries, rows_per_seq of them over each sequence's cache of `capacity` rows, as
-// kGivenItemCtas lists of items (query, first 128-key tile, tiles, part or -1 to write O).
-constexpr int kGivenItemCtas = 148;
-bool launch_sparse_attn_tc_items(int64_t rows, int rows_per_seq, const void* Q, const void* Kc, const void* Vc,
-                                 const int32_t* idx, int64_t capacity, int k, int H, int d, float scale,
-                                 const int4* items, const int* cta_items, void* O, float* Opart, float* mpart,
-                                 float* lpart, cudaStream_t s);
-
 // Per-head RMS norm and rotation of queries [L][H][d] and keys [L][d] (either may be null).
 void launch_qk_norm_rope(int64_t L, int H, int d, const void* Q, int64_t q_stride, const void* K, int64_t k_stride,
                          const void* qw, const void* kw, float eps, const float* inv_freq, int rot, bool interleaved,
@@ -106,12 +98,15 @@ struct TreeArgs {
   uint32_t* pairs;                 // [rows * m]: node << 16 | slot
   int4* items;                     // (first key row, first pair, pairs | key rows << 16, sequence << 3 | 128-row piece)
   int* counters;                   // [2]: items, pairs
-  // the attention's work: items and each CTA's first (see launch_sparse_attn_tc_items), and of each row
-  // its first part and how many (0: nothing kept, 1: none, the row is written whole)
+  // the attention's work: items (row, first tile | tiles << 8 | kept rows << 16, part or -1 to write O whole, -)
+  // and each CTA's first; of each row its first part and how many (0: nothing kept, 1: written whole), and
+  // whether its weights left the range of the first pass
   int4* attn_items;
-  int* cta_items;                  // [kGivenItemCtas + 1]
+  int* cta_items;                  // [kTreeAttnCtas + 1]
   int2* row_parts;                 // [rows]
+  int* flags;                      // [rows]
 };
+constexpr int kTreeAttnCtas = 148;  // one per SM
 // Does the selection of a query at position t need token scores?
 HSA_DEV bool needs_scores(int64_t t, int B, int m, int k) {
   const int64_t nb = t / B + 1;
@@ -125,8 +120,12 @@ bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStrea
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s);
 bool launch_tree_token_scores(const TreeArgs& a, int batch, int d_idx, int64_t max_items, cudaStream_t s);
 void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s);
-void launch_tree_combine(const TreeArgs& a, int64_t rows, int H, const float* Opart, const float* mpart,
-                         const float* lpart, void* O, cudaStream_t s);
+bool launch_tree_attn(const TreeArgs& t, const void* Q, const int32_t* idx, int H, float scale, void* O, float* Opart,
+                      float* mpart, float* lpart, cudaStream_t s);
+void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const int32_t* idx, int H, float scale,
+                         const float* Opart, const float* mpart, const float* lpart, void* O, cudaStream_t s);
+int tree_attn_wait_flag(bool reset);
+bool tree_attn_set_inject(bool on);
 void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,
                         const int32_t* paths, const int32_t* accepted, void* k_idx_cache, void* K_cache,
                         void* V_cache, float* ksum_cache, cudaStream_t s);

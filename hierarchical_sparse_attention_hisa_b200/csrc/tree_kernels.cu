@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(int T, int64_t capacity,
 // take their keys from the tail's scores here.
 //
 // Attention: one more CTA cuts all rows' 128-key tiles, in row order, into
-// kGivenItemCtas equal shares (what a row keeps follows from its position
+// kTreeAttnCtas equal shares (what a row keeps follows from its position
 // alone). A static row per CTA leaves most SMs idle when trees are ragged; with
 // equal shares at most two rows of a CTA are cut, whose parts are combined.
 // ---------------------------------------------------------------------------
@@ -77,43 +77,46 @@ constexpr int kListNT = 512;
 
 HSA_DEV void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
   const int tid = threadIdx.x;
-  auto tiles_of = [&](int64_t row) -> int {
+  auto kept_of = [&](int64_t row) -> int {
     if (row >= rows) return 0;
     const int64_t t = a.rowpos[row];
     if (t < 0) return 0;
     const int64_t nb = t / a.B + 1;
     const int64_t n = nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1;
-    return int((min(n, int64_t(a.k)) + 127) / 128);
+    return int(min(n, int64_t(a.k)));
   };
   int64_t total = 0;
   for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
     int sum;
-    block_exclusive_scan<kListNT>(tiles_of(r0 + tid), s_tmp, &sum);
+    block_exclusive_scan<kListNT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
     total += sum;
   }
-  const int64_t quota = max(int64_t(1), (total + kGivenItemCtas - 1) / kGivenItemCtas);
+  const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
   int64_t tile0 = 0;
   int item0 = 0, part0 = 0;
   for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
     const int64_t row = r0 + tid;
-    const int n = tiles_of(row);
+    const int kept = kept_of(row), n = (kept + 127) / 128;
     int sum, items, parts;
     const int64_t s = tile0 + block_exclusive_scan<kListNT>(n, s_tmp, &sum);
     const int64_t c0 = s / quota;
     const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
     int at = item0 + block_exclusive_scan<kListNT>(pieces, s_tmp, &items);
     const int part = part0 + block_exclusive_scan<kListNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
-    if (row < rows) a.row_parts[row] = make_int2(part, pieces);
+    if (row < rows) {
+      a.row_parts[row] = make_int2(part, pieces);
+      a.flags[row] = 0;
+    }
     for (int j = 0; j < pieces; ++j, ++at) {
       const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
-      a.attn_items[at] = make_int4(int(row), int(lo - s), int(hi - lo), pieces > 1 ? part + j : -1);
+      a.attn_items[at] = make_int4(int(row), int(lo - s) | int(hi - lo) << 8 | kept << 16, pieces > 1 ? part + j : -1, 0);
       if (lo == (c0 + j) * quota) a.cta_items[c0 + j] = at;  // the first item of CTA c0 + j
     }
     tile0 += sum;
     item0 += items;
     part0 += parts;
   }
-  for (int64_t c = (total + quota - 1) / quota + tid; c <= kGivenItemCtas; c += kListNT) a.cta_items[c] = item0;
+  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += kListNT) a.cta_items[c] = item0;
 }
 
 __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, int64_t rows, int ranges) {
@@ -225,19 +228,99 @@ __global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int64_
   }
 }
 
-// O of the rows that were cut (with M the largest part maximum, O = sum_p
-// 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), and of the rows that
-// keep nothing (zero). Grid (row, head groups), a thread per four values; the
-// parts come eight at a time, every load of a group issued before any is used.
+// The softmax of one row whose weights left the range that the attention's
+// fixed reference covers, on CUDA cores with a running maximum: a warp per head
+// (HPC heads per CTA), 128 kept rows at a time. A lane scores four rows, then
+// holds D / 32 output values.
 template <int D>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int H, const float* __restrict__ Opart,
+__device__ void attend_row(const TreeArgs& a, int64_t row, const uint16_t* Q, const int32_t* idx, int H, int h0, int h1,
+                           float scale, float (*p_s)[128], uint16_t* O) {
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t b = row / a.T, base = b * a.capacity;
+  const int64_t t = a.rowpos[row];
+  const int64_t nb = t / a.B + 1;
+  const int n = int(min(int64_t(a.k), nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1));
+  for (int h = h0 + warp; h < h1; h += 8) {
+    const uint4* q = reinterpret_cast<const uint4*>(Q + (row * H + h) * D);
+    float M = -INFINITY, l = 0.f, o[V] = {};
+    for (int c0 = 0; c0 < n; c0 += 128) {
+      float x[4], top = -INFINITY;
+      bool bad = false;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = c0 + 32 * u + lane;
+        x[u] = -INFINITY;
+        if (c < n) {
+          const uint4* kr = reinterpret_cast<const uint4*>(a.K_cache + (base + max(idx[row * a.k + c], 0)) * D);
+          float acc = 0.f;
+          for (int e = 0; e < D / 8; ++e) {
+            const uint4 kv = kr[e], qv = __ldg(q + e);
+            acc = __fmaf_rn(bf16_lo(qv.x), bf16_lo(kv.x), acc); acc = __fmaf_rn(bf16_hi(qv.x), bf16_hi(kv.x), acc);
+            acc = __fmaf_rn(bf16_lo(qv.y), bf16_lo(kv.y), acc); acc = __fmaf_rn(bf16_hi(qv.y), bf16_hi(kv.y), acc);
+            acc = __fmaf_rn(bf16_lo(qv.z), bf16_lo(kv.z), acc); acc = __fmaf_rn(bf16_hi(qv.z), bf16_hi(kv.z), acc);
+            acc = __fmaf_rn(bf16_lo(qv.w), bf16_lo(kv.w), acc); acc = __fmaf_rn(bf16_hi(qv.w), bf16_hi(kv.w), acc);
+          }
+          x[u] = acc * scale;
+          bad = bad || x[u] != x[u];
+        }
+        top = fmaxf(top, x[u]);
+      }
+#pragma unroll
+      for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
+      const float Mn = fmaxf(M, top), ref = Mn == -INFINITY ? 0.f : Mn;
+      const float g = M == -INFINITY ? 0.f : expf(M - ref);
+      float add = bad ? NAN : 0.f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float p = expf(x[u] - ref);
+        add += p;
+        p_s[warp][32 * u + lane] = p;
+      }
+#pragma unroll
+      for (int s = 16; s >= 1; s >>= 1) add += __shfl_xor_sync(kFull, add, s);
+      l = l * g + add;
+      M = Mn;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] *= g;
+      __syncwarp();
+      for (int c = c0; c < min(n, c0 + 128); ++c) {
+        const float p = p_s[warp][c - c0];
+        const uint16_t* vr = a.V_cache + (base + max(idx[row * a.k + c], 0)) * D + lane * V;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = __fmaf_rn(p, __uint_as_float(uint32_t(vr[e]) << 16), o[e]);
+      }
+      __syncwarp();
+    }
+    // (every score -inf: no weights at all, as a row that keeps nothing)
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int e = 0; e < V; ++e) O[(row * H + h) * D + lane * V + e] = uint16_t(f32_to_bf16_rn(o[e] * inv));
+  }
+}
+
+// O of the rows that were cut (with M the largest part maximum, O = sum_p
+// 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), of the rows that keep
+// nothing (zero), and of the flagged ones (taken again). Grid (row, head
+// groups), a thread per four values; the parts come eight at a time, every load
+// of a group issued before any is used.
+template <int D>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, const uint16_t* __restrict__ Q,
+                                                           const int32_t* __restrict__ idx, int H, float scale,
+                                                           const float* __restrict__ Opart,
                                                            const float* __restrict__ mpart,
                                                            const float* __restrict__ lpart, uint16_t* __restrict__ O) {
   constexpr int TPH = D / 4, HPC = 256 / TPH, U = 8;  // threads per head, heads per CTA at a time
+  __shared__ float p_s[8][128];
   griddep_wait();
   griddep_launch();
   const int64_t row = blockIdx.x;
   const int2 rp = a.row_parts[row];
+  if (a.flags[row]) {
+    for (int h = blockIdx.y * HPC; h < H; h += gridDim.y * HPC)
+      attend_row<D>(a, row, Q, idx, H, h, min(H, h + HPC), scale, p_s, O);
+    return;
+  }
   if (rp.y == 1) return;  // written whole
   const int v = threadIdx.x % TPH;
   for (int h = blockIdx.y * HPC + threadIdx.x / TPH; h < H; h += gridDim.y * HPC) {
@@ -256,22 +339,18 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int
       }
       float top = M;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (l[u] > 0.f) top = fmaxf(top, m[u]);
-      if (p0 > 0) {
-        const float g = top == -INFINITY ? 1.f : exp2f(M - top);
-        num.x *= g; num.y *= g; num.z *= g; num.w *= g;
-        den *= g;
-      }
+      for (int u = 0; u < U; ++u) top = fmaxf(top, m[u]);
+      const float g = p0 > 0 ? exp2f(M - top) : 1.f;  // (a row not flagged has finite maxima)
+      num.x *= g; num.y *= g; num.z *= g; num.w *= g;
+      den *= g;
       M = top;
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (l[u] > 0.f) {  // an empty part has no weight, and nothing in its O
-          const float g = exp2f(m[u] - M);
-          num.x = __fmaf_rn(g, o[u].x, num.x); num.y = __fmaf_rn(g, o[u].y, num.y);
-          num.z = __fmaf_rn(g, o[u].z, num.z); num.w = __fmaf_rn(g, o[u].w, num.w);
-          den = __fmaf_rn(g, l[u], den);
-        }
+      for (int u = 0; u < U; ++u) {
+        const float f = exp2f(m[u] - M);
+        num.x = __fmaf_rn(f, o[u].x, num.x); num.y = __fmaf_rn(f, o[u].y, num.y);
+        num.z = __fmaf_rn(f, o[u].z, num.z); num.w = __fmaf_rn(f, o[u].w, num.w);
+        den = __fmaf_rn(f, l[u], den);
+      }
     }
     const float inv = den > 0.f ? 1.f / den : 0.f;
     reinterpret_cast<uint2*>(O + (row * H + h) * D)[v] =
@@ -386,14 +465,14 @@ void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_
   launch_kernel(true, tree_rows_kernel, unsigned((rows + 7) / 8), 256, 0, s, a, rows, idx);
 }
 
-void launch_tree_combine(const TreeArgs& a, int64_t rows, int H, const float* Opart, const float* mpart,
-                         const float* lpart, void* O, cudaStream_t s) {
+void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const int32_t* idx, int H, float scale,
+                         const float* Opart, const float* mpart, const float* lpart, void* O, cudaStream_t s) {
   // a CTA per head group, fewer when the rows alone make a large grid (most of a large call's rows were written whole)
   const int64_t groups = std::min<int64_t>((H * a.d + 1023) / 1024, std::max<int64_t>(1, 16384 / rows));
   const dim3 grid{unsigned(rows), unsigned(groups)};
   count_launches(1);
-  launch_kernel(true, a.d == 128 ? tree_combine_kernel<128> : tree_combine_kernel<64>, grid, 256, 0, s, a, H, Opart,
-                mpart, lpart, (uint16_t*)O);
+  launch_kernel(true, a.d == 128 ? tree_combine_kernel<128> : tree_combine_kernel<64>, grid, 256, 0, s, a,
+                (const uint16_t*)Q, idx, H, scale, Opart, mpart, lpart, (uint16_t*)O);
 }
 
 void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,

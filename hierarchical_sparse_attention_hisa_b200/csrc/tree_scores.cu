@@ -20,19 +20,33 @@ using namespace tc;
 
 constexpr long long kInjectWaitCycles = 1ll << 21;  // about a millisecond
 
+HSA_DEV void tmem_ld1(uint32_t taddr, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+}
+
+// Bounded wait; the limit, the error flag and the test hook are slow to read, so
+// they are looked at once in 64 probes.
 HSA_DEV bool tw_wait(uint64_t* bar, uint32_t parity, bool& dead) {
   if (dead) return false;
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long lim = *(volatile int*)&g_tree_inject ? kInjectWaitCycles : kWaitCycles;
-  if (mbar_wait_bounded(bar, parity, &g_tree_err, lim)) return true;
+  long long t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*(volatile int*)&g_tree_err) break;
+      const long long t = clock64();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > (*(volatile int*)&g_tree_inject ? kInjectWaitCycles : kWaitCycles)) {
+        atomicExch(&g_tree_err, 1);
+        break;
+      }
+    }
+  }
   dead = true;
   return false;
 }
+// Every lane polls (a lane that polls for the others holds the warp up).
 HSA_DEV bool tw_wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
-  bool ok = false;
-  if ((threadIdx.x & 31) == 0) ok = tw_wait(bar, parity, dead);
-  ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-  __syncwarp();
+  const bool ok = __all_sync(kFull, tw_wait(bar, parity, dead));
   dead = !ok;
   return ok;
 }

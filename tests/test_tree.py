@@ -207,6 +207,11 @@ STEP_CASES = {
     "rows_200": dict(SMALL, ctx=[950, 800, 700, 650, 600], T=40, capacity=1024, kind="binary"),
     "wide_rows": dict(B=64, m=300, k=1000, d_idx=64, H=4, d=64, ctx=[30000, 20095], T=6, capacity=32768),
     "scaled": dict(SMALL, ctx=[900], T=6, capacity=1024, scale=0.7),
+    # logits hundreds of nats apart: weights that leave the range of a list's first tile
+    "hot": dict(B=64, m=16, k=700, d_idx=64, H=20, d=64, ctx=[1900, 1500], T=9, capacity=2048, scale=8.0),
+    "hot_wide": dict(B=128, m=8, k=1000, d_idx=128, H=70, d=128, ctx=[1900, 1000], T=40, capacity=2048, scale=3.0),
+    # 4 and 64 tiles of kept rows per node
+    "long_lists": dict(B=128, m=64, k=8192, d_idx=64, H=3, d=128, ctx=[8190, 9000, 300], T=7, capacity=9216),
     # every score the same: ties go to the lowest position
     "ties": dict(SMALL, ctx=[1000, 700], T=20, capacity=1088, zero_q=True, kind="chain"),
 }
@@ -224,6 +229,26 @@ def test_step_against_oracle(hsa, name):
     import torch
     assert torch.equal(O.view(torch.int16), O2.view(torch.int16)) and torch.equal(idx, idx2)
     assert hsa.hsa_device_status(reset=False) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["ragged", "block_200", "rows_200", "many_heads"])
+def test_rows_that_are_not_kept_do_not_matter(hsa, name):
+    """NaN and infinities behind the drafted rows, and in the K and V rows that no node keeps."""
+    import torch
+    c = Case(hsa, **STEP_CASES[name])
+    O, idx = c.run()
+    for b in range(c.batch):
+        used = torch.zeros(c.capacity, dtype=torch.bool, device="cuda")
+        rows = idx[b][idx[b] >= 0].long()
+        used[rows] = True
+        n = int((c.pos[b] >= 0).sum())
+        behind = torch.arange(c.capacity, device="cuda") >= int(c.ctx[b]) + n
+        c.g["kc"][b, behind] = float("nan")
+        for t, bad in (("Kc", float("nan")), ("Vc", float("inf"))):
+            c.g[t][b, ~used] = bad
+    O2, idx2 = c.run()
+    assert torch.equal(idx, idx2) and torch.equal(O.view(torch.int16), O2.view(torch.int16))
 
 
 @pytest.mark.gpu
