@@ -456,9 +456,10 @@ struct TreeWs {
 TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) {
   TreeWs w{};
   w.rows = int64_t(batch) * T;
-  w.ldb = capacity / p->B;
+  const int64_t blocks = capacity / p->B;
+  w.ldb = (hsa::kBkeys0 + blocks + 3) / 4 * 4;
   w.tail_ld = (p->B - 1 + T + 3) / 4 * 4;
-  w.max_items = batch * std::min<int64_t>(int64_t(T) * p->m, w.ldb) * ((p->B + 127) / 128);
+  w.max_items = batch * std::min<int64_t>(int64_t(T) * p->m, blocks) * ((p->B + 127) / 128);
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes > 0 ? bytes : 1); return at; };
   const size_t rows = size_t(w.rows);
@@ -559,18 +560,21 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   a.cta_items = reinterpret_cast<int*>(ws + w.cta);
   a.row_parts = reinterpret_cast<int2*>(ws + w.rparts);
   a.flags = reinterpret_cast<int*>(ws + w.flags);
-  // A node's row of the selections is at the node's own position; a row that
-  // takes no part has position -1.
-  hsa::RowMap rm{w.rows, capacity, a.rowpos, capacity};
   // The kernels are programmatic dependent launches, as in a decode step.
   // 1. drafted rows appended, tails and cached blocks scored; top-m
   if (!hsa::launch_tree_block_scores(a, batch, p->d_idx, stream)) return HSA_ERR_CUDA;
-  hsa::launch_topm_from_keys(rm, w.rows, a.bkeys, w.ldb, p->B, p->m, w.ldb > 2 ? w.ldb - 2 : 1, blocks, stream, true);
+  hsa::launch_tree_topm(a, w.rows, blocks, stream);
   // 2. token scores of the kept blocks, each cached block read once for all its nodes; top-k
   hsa::launch_tree_lists(a, batch, stream);
   if (!hsa::launch_tree_token_scores(a, batch, p->d_idx, w.max_items, stream)) return HSA_ERR_CUDA;
-  hsa::launch_topk_from_keys(rm, w.rows, blocks, a.tkeys, p->B, p->m, p->k, idx, stream, true);
-  hsa::launch_tree_rows(a, w.rows, idx, stream);
+  if (hsa::tree_topk_wide(a, w.rows)) {
+    hsa::launch_tree_topk(a, w.rows, idx, stream);
+  } else {
+    // a node's row of the selection is at the node's own position; a row that takes no part has position -1
+    const hsa::RowMap rm{w.rows, capacity, a.rowpos, capacity};
+    hsa::launch_topk_from_keys(rm, w.rows, blocks, a.tkeys, p->B, p->m, p->k, idx, stream, true);
+    hsa::launch_tree_rows(a, w.rows, idx, stream);
+  }
   // 3. attention over the kept rows, in equal shares of 128-key tiles per CTA
   float* opart = reinterpret_cast<float*>(ws + w.opart);
   float* mpart = reinterpret_cast<float*>(ws + w.mpart);

@@ -86,7 +86,7 @@ void launch_qk_norm_rope(int64_t L, int H, int d, const void* Q, int64_t q_strid
 constexpr int kTreeMax = HSA_TREE_MAX;
 struct TreeArgs {
   int T, B, m, k, d;
-  int64_t capacity, ldb;           // ldb: row length of bkeys
+  int64_t capacity, ldb;           // ldb: row length of bkeys (kBkeys0 keys, then the blocks' from block 0 on)
   const int32_t *ctx, *positions, *paths;
   uint16_t *k_idx_cache, *K_cache, *V_cache;
   const float* ksum_cache;
@@ -107,6 +107,8 @@ struct TreeArgs {
   int* flags;                      // [rows]
 };
 constexpr int kTreeAttnCtas = 148;  // one per SM
+constexpr int kBkeys0 = 3;          // so that block 1's key, the first candidate, is on 16 bytes
+constexpr int kWideRows = 592;      // two CTAs of 1024 threads per SM, two waves
 // Does the selection of a query at position t need token scores?
 HSA_DEV bool needs_scores(int64_t t, int B, int m, int k) {
   const int64_t nb = t / B + 1;
@@ -119,6 +121,10 @@ void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, co
 bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStream_t s);
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s);
 bool launch_tree_token_scores(const TreeArgs& a, int batch, int d_idx, int64_t max_items, cudaStream_t s);
+void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStream_t s);
+// Whether launch_tree_topk takes these rows (else launch_topk_from_keys, then launch_tree_rows).
+bool tree_topk_wide(const TreeArgs& a, int64_t rows);
+void launch_tree_topk(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s);
 void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s);
 bool launch_tree_attn(const TreeArgs& t, const void* Q, const int32_t* idx, int H, float scale, void* O, float* Opart,
                       float* mpart, float* lpart, cudaStream_t s);

@@ -60,76 +60,21 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(int T, int64_t capacity,
 }
 
 // ---------------------------------------------------------------------------
-// Work lists, one launch.
-//
-// Token scores: CTA (sequence, range of 512 cached blocks), a thread per block:
-// the (node, slot) pairs of each kept block and an item per 128 rows of such a
-// block. The order of items and of pairs inside one is not fixed (atomics);
-// each writes its own keys, so results do not depend on it. Kept tail blocks
-// take their keys from the tail's scores here.
-//
-// Attention: one more CTA cuts all rows' 128-key tiles, in row order, into
-// kTreeAttnCtas equal shares (what a row keeps follows from its position
-// alone). A static row per CTA leaves most SMs idle when trees are ragged; with
-// equal shares at most two rows of a CTA are cut, whose parts are combined.
+// Work lists of the token scores, CTA (sequence, range of 512 cached blocks), a
+// thread per block: the (node, slot) pairs of each kept block and an item per
+// 128 rows of such a block. The order of items and of pairs inside one is not
+// fixed (atomics); each writes its own keys, so results do not depend on it.
+// Kept tail blocks take their keys from the tail's scores here.
 // ---------------------------------------------------------------------------
 constexpr int kListNT = 512;
 
-HSA_DEV void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
-  const int tid = threadIdx.x;
-  auto kept_of = [&](int64_t row) -> int {
-    if (row >= rows) return 0;
-    const int64_t t = a.rowpos[row];
-    if (t < 0) return 0;
-    const int64_t nb = t / a.B + 1;
-    const int64_t n = nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1;
-    return int(min(n, int64_t(a.k)));
-  };
-  int64_t total = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
-    int sum;
-    block_exclusive_scan<kListNT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
-    total += sum;
-  }
-  const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
-  int64_t tile0 = 0;
-  int item0 = 0, part0 = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
-    const int64_t row = r0 + tid;
-    const int kept = kept_of(row), n = (kept + 127) / 128;
-    int sum, items, parts;
-    const int64_t s = tile0 + block_exclusive_scan<kListNT>(n, s_tmp, &sum);
-    const int64_t c0 = s / quota;
-    const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
-    int at = item0 + block_exclusive_scan<kListNT>(pieces, s_tmp, &items);
-    const int part = part0 + block_exclusive_scan<kListNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
-    if (row < rows) {
-      a.row_parts[row] = make_int2(part, pieces);
-      a.flags[row] = 0;
-    }
-    for (int j = 0; j < pieces; ++j, ++at) {
-      const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
-      a.attn_items[at] = make_int4(int(row), int(lo - s) | int(hi - lo) << 8 | kept << 16, pieces > 1 ? part + j : -1, 0);
-      if (lo == (c0 + j) * quota) a.cta_items[c0 + j] = at;  // the first item of CTA c0 + j
-    }
-    tile0 += sum;
-    item0 += items;
-    part0 += parts;
-  }
-  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += kListNT) a.cta_items[c] = item0;
-}
-
-__global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, int64_t rows, int ranges) {
+__global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, int ranges) {
   __shared__ int hist[kListNT];  // pair counts of this range's blocks, then cursors
   __shared__ int s_tmp[kListNT / 32 + 1];
   __shared__ int s_base[2];
   __shared__ int pos_s[kTreeMax];
   griddep_wait();
   griddep_launch();
-  if (blockIdx.x == gridDim.x - 1) {
-    attn_shares(a, rows, s_tmp);
-    return;
-  }
   const int64_t b = blockIdx.x / ranges;
   const int range = int(blockIdx.x % ranges);
   const int64_t c = a.ctx[b];
@@ -201,6 +146,83 @@ __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, i
     const int i = e / a.m;
     pairs[atomicAdd(&hist[blk - lo], 1)] = uint32_t(i) << 16 | uint32_t(e - i * a.m);
   });
+}
+
+// ---------------------------------------------------------------------------
+// Selections with a wide CTA per row, keys in registers (RegSelect): what a
+// step's latency needs, where the prefill's kernels are made for many rows.
+// At most kWideRows rows are one wave of the device.
+//
+// Top-m: candidate c is block c + 1 of 1 .. nb-2; bkeys rows start three keys
+// in, so that block 1's key is on 16 bytes.
+// ---------------------------------------------------------------------------
+template <int NT, int KPT>
+__global__ void __launch_bounds__(NT) tree_topm_kernel(const TreeArgs a, int32_t* __restrict__ blocks) {
+  __shared__ uint32_t hist[RegSelect<NT, KPT>::kBins];
+  __shared__ int scratch[NT / 32 + 8];
+  griddep_wait();
+  griddep_launch();
+  const int64_t row = blockIdx.x;
+  const int64_t t = a.rowpos[row];
+  int32_t* out = blocks + row * a.m;
+  const int64_t nb = t < 0 ? 0 : t / a.B + 1;
+  if (nb <= a.m) {
+    for (int s = threadIdx.x; s < a.m; s += NT) out[s] = s < nb ? s : -1;
+    return;
+  }
+  if (threadIdx.x == 0) { out[0] = 0; out[a.m - 1] = int32_t(nb - 1); }
+  if (a.m == 2) return;
+  const int n = int(nb - 2);
+  uint32_t key[KPT];
+  load_keys<KPT>(a.bkeys + row * a.ldb + kBkeys0 + 1, n, key);
+  RegSelect<NT, KPT> rs{hist, scratch};
+  uint32_t T;
+  int take_eq;
+  rs.threshold(key, n, a.m - 2, &T, &take_eq);
+  rs.compact(key, n, T, take_eq, [&](int rank, int c) { out[1 + rank] = c + 1; });
+}
+
+// Top-k of a node's candidates (the tokens of its kept blocks, ascending), and
+// their positions as rows of the sequence's cache.
+template <int NT, int KPT>
+__global__ void __launch_bounds__(NT) tree_topk_kernel(const TreeArgs a, int32_t* __restrict__ idx) {
+  __shared__ uint32_t hist[RegSelect<NT, KPT>::kBins];
+  __shared__ int scratch[NT / 32 + 8];
+  __shared__ int blk[512];
+  __shared__ int path[kTreeMax];
+  griddep_wait();
+  griddep_launch();
+  const int64_t row = blockIdx.x;
+  const int64_t t = a.rowpos[row];
+  int32_t* out = idx + row * a.k;
+  if (t < 0) {
+    for (int s = threadIdx.x; s < a.k; s += NT) out[s] = -1;
+    return;
+  }
+  const int64_t nb = t / a.B + 1;
+  const int n = int(nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1);
+  uint32_t key[KPT];
+  if (n > a.k) load_keys<KPT>(a.tkeys + row * int64_t(a.m) * a.B, n, key);
+  for (int s = threadIdx.x; s < a.m; s += NT) blk[s] = a.blocks[row * a.m + s];
+  const int c0 = a.ctx[row / a.T];
+  if (int(threadIdx.x) <= int(t) - c0)
+    path[threadIdx.x] = min(max(a.paths[row * a.T + threadIdx.x], 0), a.T - 1);
+  __syncthreads();
+  const bool pow2 = (a.B & (a.B - 1)) == 0;
+  const int lb = 31 - __clz(a.B);
+  auto row_of = [&](int c) -> int32_t {
+    const int p = pow2 ? (blk[c >> lb] << lb) + (c & (a.B - 1)) : blk[c / a.B] * a.B + c % a.B;
+    return p < c0 ? p : c0 + path[p - c0];
+  };
+  if (n <= a.k) {
+    for (int s = threadIdx.x; s < a.k; s += NT) out[s] = s < n ? row_of(s) : -1;
+    return;
+  }
+  RegSelect<NT, KPT> rs{hist, scratch};
+  uint32_t T;
+  int take_eq;
+  rs.threshold(key, n, a.k, &T, &take_eq);
+  rs.compact(key, n, T, take_eq, [&](int rank, int c) { out[rank] = row_of(c); });
 }
 
 // Kept positions of each node -> rows of its sequence's cache, in place, a warp
@@ -301,11 +323,14 @@ __device__ void attend_row(const TreeArgs& a, int64_t row, const uint16_t* Q, co
 
 // O of the rows that were cut (with M the largest part maximum, O = sum_p
 // 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), of the rows that keep
-// nothing (zero), and of the flagged ones (taken again). Grid (row, head
+// nothing (zero), and of the flagged ones (taken again). Grid (rows / 4, head
 // groups), a thread per four values; the parts come eight at a time, every load
-// of a group issued before any is used.
+// of a group issued before any is used. Most rows of a large call were written
+// whole: a CTA looks four up at once (one each: 4096 CTAs, 12 us for 512 rows).
+constexpr int kCombineRows = 4;
 template <int D>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, const uint16_t* __restrict__ Q,
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int64_t rows, int rows_per_cta,
+                                                           const uint16_t* __restrict__ Q,
                                                            const int32_t* __restrict__ idx, int H, float scale,
                                                            const float* __restrict__ Opart,
                                                            const float* __restrict__ mpart,
@@ -314,15 +339,26 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, con
   __shared__ float p_s[8][128];
   griddep_wait();
   griddep_launch();
-  const int64_t row = blockIdx.x;
-  const int2 rp = a.row_parts[row];
-  if (a.flags[row]) {
+  const int v = threadIdx.x % TPH;
+  int2 parts[kCombineRows];
+  int flag[kCombineRows];
+#pragma unroll
+  for (int i = 0; i < kCombineRows; ++i) {
+    const int64_t row = int64_t(blockIdx.x) * rows_per_cta + i;
+    const bool in = i < rows_per_cta && row < rows;
+    parts[i] = in ? a.row_parts[row] : make_int2(0, 1);
+    flag[i] = in ? a.flags[row] : 0;
+  }
+#pragma unroll
+  for (int i = 0; i < kCombineRows; ++i) {
+  const int64_t row = int64_t(blockIdx.x) * rows_per_cta + i;
+  const int2 rp = parts[i];
+  if (flag[i]) {
     for (int h = blockIdx.y * HPC; h < H; h += gridDim.y * HPC)
       attend_row<D>(a, row, Q, idx, H, h, min(H, h + HPC), scale, p_s, O);
-    return;
+    continue;
   }
-  if (rp.y == 1) return;  // written whole
-  const int v = threadIdx.x % TPH;
+  if (rp.y == 1) continue;  // written whole
   for (int h = blockIdx.y * HPC + threadIdx.x / TPH; h < H; h += gridDim.y * HPC) {
     float M = -INFINITY, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -355,6 +391,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, con
     const float inv = den > 0.f ? 1.f / den : 0.f;
     reinterpret_cast<uint2*>(O + (row * H + h) * D)[v] =
         make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
+  }
   }
 }
 
@@ -457,7 +494,32 @@ void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, co
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s) {
   const int ranges = int((a.capacity / a.B + kListNT - 1) / kListNT);
   count_launches(1);
-  launch_kernel(true, tree_lists_kernel, unsigned(batch * ranges + 1), kListNT, 0, s, a, int64_t(batch) * a.T, ranges);
+  launch_kernel(true, tree_lists_kernel, unsigned(batch * ranges), kListNT, 0, s, a, ranges);
+}
+
+void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStream_t s) {
+  const int64_t n = a.capacity / a.B;
+  count_launches(1);
+  auto go = [&](auto kern, int nt) { launch_kernel(true, kern, unsigned(rows), nt, 0, s, a, blocks); };
+  if (n <= 256) go(tree_topm_kernel<256, 1>, 256);
+  else if (n <= 1024) go(tree_topm_kernel<256, 4>, 256);
+  else if (n <= 2048) go(tree_topm_kernel<512, 4>, 512);
+  else if (n <= 4096) go(tree_topm_kernel<1024, 4>, 1024);
+  else if (n <= 8192) go(tree_topm_kernel<1024, 8>, 1024);
+  else go(tree_topm_kernel<1024, 16>, 1024);  // (at most 16384 blocks)
+}
+
+bool tree_topk_wide(const TreeArgs& a, int64_t rows) { return rows <= kWideRows && int64_t(a.m) * a.B <= 16384; }
+
+void launch_tree_topk(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s) {
+  const int64_t n = int64_t(a.m) * a.B;
+  count_launches(1);
+  auto go = [&](auto kern, int nt) { launch_kernel(true, kern, unsigned(rows), nt, 0, s, a, idx); };
+  if (n <= 256) go(tree_topk_kernel<256, 1>, 256);
+  else if (n <= 1024) go(tree_topk_kernel<256, 4>, 256);
+  else if (n <= 4096) go(tree_topk_kernel<1024, 4>, 1024);
+  else if (n <= 8192) go(tree_topk_kernel<1024, 8>, 1024);
+  else go(tree_topk_kernel<1024, 16>, 1024);
 }
 
 void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s) {
@@ -467,11 +529,13 @@ void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_
 
 void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const int32_t* idx, int H, float scale,
                          const float* Opart, const float* mpart, const float* lpart, void* O, cudaStream_t s) {
-  // a CTA per head group, fewer when the rows alone make a large grid (most of a large call's rows were written whole)
-  const int64_t groups = std::min<int64_t>((H * a.d + 1023) / 1024, std::max<int64_t>(1, 16384 / rows));
-  const dim3 grid{unsigned(rows), unsigned(groups)};
+  // a CTA per head group, fewer when the rows alone make a large grid
+  const int per = rows > 2 * num_sms() ? kCombineRows : 1;
+  const int64_t ctas = (rows + per - 1) / per;
+  const int64_t groups = std::min<int64_t>((H * a.d + 1023) / 1024, std::max<int64_t>(1, 8192 / ctas));
+  const dim3 grid{unsigned(ctas), unsigned(groups)};
   count_launches(1);
-  launch_kernel(true, a.d == 128 ? tree_combine_kernel<128> : tree_combine_kernel<64>, grid, 256, 0, s, a,
+  launch_kernel(true, a.d == 128 ? tree_combine_kernel<128> : tree_combine_kernel<64>, grid, 256, 0, s, a, rows, per,
                 (const uint16_t*)Q, idx, H, scale, Opart, mpart, lpart, (uint16_t*)O);
 }
 

@@ -72,6 +72,13 @@ HSA_DEV bool tw_wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
 constexpr int kBlkTile = 128;
 constexpr int kNT = 256, kNodeNT = 128, kNodesPerCta = kNT / kNodeNT;
 
+// Node i's position, or -1 if it takes no part. A plan made for other lengths
+// must not reach outside the sequence's rows.
+HSA_DEV int64_t node_position(const TreeArgs& a, int64_t b, int i) {
+  const int64_t c = a.ctx[b], t = a.positions[b * a.T + i];
+  return c >= 0 && t >= c && t - c <= i && c + i < a.capacity ? t : -1;
+}
+
 HSA_DEV float dot8(const uint4& kv, const float (&q)[8]) {
   float acc = q[0] * bf16_lo(kv.x);
   acc = __fmaf_rn(q[1], bf16_hi(kv.x), acc);
@@ -84,16 +91,61 @@ HSA_DEV float dot8(const uint4& kv, const float (&q)[8]) {
   return acc;
 }
 
+// The attention's work: all rows' 128-key tiles, in row order, cut into
+// kTreeAttnCtas equal shares (what a row keeps follows from its position
+// alone). A row per CTA leaves most SMs idle when trees are ragged; with equal
+// shares at most two rows of a CTA are cut, whose parts are combined.
+__device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
+  const int tid = threadIdx.x;
+  auto kept_of = [&](int64_t row) -> int {
+    const int64_t t = row < rows ? node_position(a, row / a.T, int(row % a.T)) : -1;
+    if (t < 0) return 0;
+    const int64_t nb = t / a.B + 1;
+    const int64_t n = nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1;
+    return int(min(n, int64_t(a.k)));
+  };
+  int64_t total = 0;
+  for (int64_t r0 = 0; r0 < rows; r0 += kNT) {
+    int sum;
+    block_exclusive_scan<kNT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
+    total += sum;
+  }
+  const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
+  int64_t tile0 = 0;
+  int item0 = 0, part0 = 0;
+  for (int64_t r0 = 0; r0 < rows; r0 += kNT) {
+    const int64_t row = r0 + tid;
+    const int kept = kept_of(row), n = (kept + 127) / 128;
+    int sum, items, parts;
+    const int64_t s = tile0 + block_exclusive_scan<kNT>(n, s_tmp, &sum);
+    const int64_t c0 = s / quota;
+    const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
+    int at = item0 + block_exclusive_scan<kNT>(pieces, s_tmp, &items);
+    const int part = part0 + block_exclusive_scan<kNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
+    if (row < rows) {
+      a.row_parts[row] = make_int2(part, pieces);
+      a.flags[row] = 0;
+    }
+    for (int j = 0; j < pieces; ++j, ++at) {
+      const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
+      a.attn_items[at] = make_int4(int(row), int(lo - s) | int(hi - lo) << 8 | kept << 16, pieces > 1 ? part + j : -1, 0);
+      if (lo == (c0 + j) * quota) a.cta_items[c0 + j] = at;  // the first item of CTA c0 + j
+    }
+    tile0 += sum;
+    item0 += items;
+    part0 += parts;
+  }
+  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += kNT) a.cta_items[c] = item0;
+}
+
 // tid: 0 .. kNodeNT-1 within the node's warps; bar: their named barrier; sc: tail_ld floats
 template <int DI>
 __device__ void node_tail(const TreeArgs& a, int64_t b, int i, int tid, int bar, float* sc) {
   const int64_t row = b * a.T + i;
   const int64_t c = a.ctx[b];
-  const int64_t t = a.positions[row];
-  // a plan made for other lengths must not reach outside the sequence's rows
-  const bool ok = c >= 0 && t >= c && t - c <= i && c + i < a.capacity;
-  if (tid == 0) a.rowpos[row] = ok ? int32_t(t) : -1;
-  if (!ok) return;
+  const int64_t t = node_position(a, b, i);
+  if (tid == 0) a.rowpos[row] = int32_t(t);
+  if (t < 0) return;
   const int lane = tid & 31, warp = tid >> 5;
   {  // the drafted rows, node i in cache row c + i
     const int64_t at = b * a.capacity + c + i;
@@ -159,7 +211,7 @@ __device__ void node_tail(const TreeArgs& a, int64_t b, int i, int tid, int bar,
     for (int r = lane; r < a.B; r += 32) s += sc[(blk - f) * a.B + r];
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-    if (lane == 0) a.bkeys[row * a.ldb + blk] = score_key(s);
+    if (lane == 0) a.bkeys[row * a.ldb + kBkeys0 + blk] = score_key(s);
   }
 }
 
@@ -251,7 +303,7 @@ __device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint
     const int r = (warp & 3) * 32 + lane, n0 = (warp >> 2) * NH;
     float v[NH];
     tmem_load_f32<NH>(tmem + (uint32_t((warp & 3) * 32) << 16) + n0, v);
-    uint32_t* out = a.bkeys + b * a.T * a.ldb + lo + r;
+    uint32_t* out = a.bkeys + b * a.T * a.ldb + kBkeys0 + lo + r;
     if (r < n) {
 #pragma unroll
       for (int i = 0; i < NH; ++i)
@@ -267,12 +319,18 @@ __device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint
 }
 
 template <int DI>
-__global__ void __launch_bounds__(kNT) tree_tails_kernel(const TreeArgs a) {
+__global__ void __launch_bounds__(kNT) tree_tails_kernel(const TreeArgs a, int64_t rows) {
   extern __shared__ __align__(16) float tail_smem[];
+  __shared__ int s_tmp[kNT / 32 + 1];
   griddep_wait();
   griddep_launch();
+  if (blockIdx.y == gridDim.y - 1) {  // one CTA more: the lists' counters, the attention's shares
+    if (blockIdx.x > 0) return;
+    if (threadIdx.x < 2) a.counters[threadIdx.x] = 0;
+    attn_shares(a, rows, s_tmp);
+    return;
+  }
   const int64_t b = blockIdx.x;
-  if (b == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
   const int half = threadIdx.x / kNodeNT, i = int(blockIdx.y) * kNodesPerCta + half;
   if (i < a.T) node_tail<DI>(a, b, i, threadIdx.x % kNodeNT, 1 + half, tail_smem + half * a.tail_ld);
 }
@@ -473,8 +531,8 @@ bool launch_bs(const TreeArgs& a, int batch, cudaStream_t s) {
   auto blocks = tree_block_scores_kernel<DI, N>;
   if (cudaFuncSetAttribute(blocks, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_b) != cudaSuccess) return false;
   count_launches(2);
-  launch_kernel(true, tree_tails_kernel<DI>, dim3(unsigned(batch), unsigned((a.T + kNodesPerCta - 1) / kNodesPerCta)),
-                kNT, size_t(smem_t), s, a);
+  launch_kernel(true, tree_tails_kernel<DI>, dim3(unsigned(batch), unsigned((a.T + kNodesPerCta - 1) / kNodesPerCta + 1)),
+                kNT, size_t(smem_t), s, a, int64_t(batch) * a.T);
   launch_kernel(true, blocks, dim3(unsigned(batch), unsigned(tiles)), kNT, size_t(smem_b), s, a);
   return true;
 }
