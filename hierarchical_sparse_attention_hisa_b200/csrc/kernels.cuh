@@ -109,12 +109,8 @@ struct TreeArgs {
 constexpr int kTreeAttnCtas = 148;  // one per SM
 constexpr int kBkeys0 = 3;          // so that block 1's key, the first candidate, is on 16 bytes
 constexpr int kWideRows = 592;      // two CTAs of 1024 threads per SM, two waves
-// Does the selection of a query at position t need token scores?
-HSA_DEV bool needs_scores(int64_t t, int B, int m, int k) {
-  const int64_t nb = t / B + 1;
-  const int64_t n = nb <= m ? t + 1 : int64_t(m - 1) * B + t % B + 1;
-  return n > k;
-}
+// Token candidates of a query at position t: all up to it, or those of its m kept blocks.
+HSA_DEV int candidates(int t, int B, int m) { return t / B < m ? t + 1 : (m - 1) * B + t % B + 1; }
 void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, const int32_t* n_nodes,
                       const int32_t* parents, int32_t* positions, int32_t* paths, cudaStream_t s);
 // (also appends the drafted rows to the caches and scores every node's tail)

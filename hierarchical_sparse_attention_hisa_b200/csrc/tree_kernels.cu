@@ -64,83 +64,143 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(int T, int64_t capacity,
 // thread per block: the (node, slot) pairs of each kept block and an item per
 // 128 rows of such a block. The order of items and of pairs inside one is not
 // fixed (atomics); each writes its own keys, so results do not depend on it.
-// Kept tail blocks take their keys from the tail's scores here.
+//
+// Beside them, a CTA per sequence gives the kept tail blocks their keys from the
+// tail's scores, and one CTA cuts the attention's work.
 // ---------------------------------------------------------------------------
 constexpr int kListNT = 512;
 
-__global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, int ranges) {
+// The attention's work: all rows' 128-key tiles, in row order, cut into
+// kTreeAttnCtas equal shares (what a row keeps follows from its position
+// alone). A row per CTA leaves most SMs idle when trees are ragged; with equal
+// shares at most two rows of a CTA are cut, whose parts are combined.
+__device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
+  const int tid = threadIdx.x;
+  auto kept_of = [&](int64_t row) -> int {
+    const int t = row < rows ? a.rowpos[row] : -1;
+    if (t < 0) return 0;
+    return min(a.k, candidates(t, a.B, a.m));
+  };
+  int64_t total = 0;
+  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
+    int sum;
+    block_exclusive_scan<kListNT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
+    total += sum;
+  }
+  const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
+  int64_t tile0 = 0;
+  int item0 = 0, part0 = 0;
+  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
+    const int64_t row = r0 + tid;
+    const int kept = kept_of(row), n = (kept + 127) / 128;
+    int sum, items, parts;
+    const int64_t s = tile0 + block_exclusive_scan<kListNT>(n, s_tmp, &sum);
+    const int64_t c0 = s / quota;
+    const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
+    int at = item0 + block_exclusive_scan<kListNT>(pieces, s_tmp, &items);
+    const int part = part0 + block_exclusive_scan<kListNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
+    if (row < rows) {
+      a.row_parts[row] = make_int2(part, pieces);
+      a.flags[row] = 0;
+    }
+    for (int j = 0; j < pieces; ++j, ++at) {
+      const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
+      a.attn_items[at] = make_int4(int(row), int(lo - s) | int(hi - lo) << 8 | kept << 16, pieces > 1 ? part + j : -1, 0);
+      if (lo == (c0 + j) * quota) a.cta_items[c0 + j] = at;  // the first item of CTA c0 + j
+    }
+    tile0 += sum;
+    item0 += items;
+    part0 += parts;
+  }
+  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += kListNT) a.cta_items[c] = item0;
+}
+
+__device__ void tail_keys(const TreeArgs& a, int64_t b) {
+  const int64_t c = a.ctx[b];
+  if (c < 0 || c >= a.capacity) return;
+  const int f = int(c / a.B), lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < a.T; i += kListNT / 32) {  // a warp per node
+    const int64_t row = b * a.T + i;
+    const int t = a.rowpos[row];
+    if (t < 0 || candidates(t, a.B, a.m) <= a.k) continue;
+    const int nb = t / a.B + 1, n = t - f * a.B + 1;  // n: the node's tail rows
+    const int nblk = min(a.m, nb);
+    const uint32_t* src = a.tailkeys + row * a.tail_ld;
+    // the kept tail blocks are the last of the list, 32 looked up at a time
+    for (int s0 = nblk - 1; s0 >= 0; s0 -= 32) {
+      const int mine = s0 - lane >= 0 ? a.blocks[row * a.m + s0 - lane] : -1;
+      const int cnt = __popc(__ballot_sync(kFull, mine >= f));
+      for (int u = 0; u < cnt; ++u) {
+        const int r0 = (__shfl_sync(kFull, mine, u) - f) * a.B;
+        uint32_t* dst = a.tkeys + (row * a.m + s0 - u) * int64_t(a.B);
+        for (int r = lane; r < a.B && r0 + r < n; r += 32) dst[r] = src[r0 + r];
+      }
+      if (cnt < 32) break;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, int batch, int ranges) {
   __shared__ int hist[kListNT];  // pair counts of this range's blocks, then cursors
   __shared__ int s_tmp[kListNT / 32 + 1];
   __shared__ int s_base[2];
-  __shared__ int pos_s[kTreeMax];
+  __shared__ uint8_t need[kTreeMax];
   griddep_wait();
   griddep_launch();
-  const int64_t b = blockIdx.x / ranges;
-  const int range = int(blockIdx.x % ranges);
-  const int64_t c = a.ctx[b];
-  if (c < 0 || c >= a.capacity) return;
-  const int f = int(c / a.B);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int lo = range * kListNT, mine = lo + tid;  // this thread's block
-  if (tid < a.T) {
-    const int t = a.rowpos[b * a.T + tid];
-    pos_s[tid] = t >= 0 && needs_scores(t, a.B, a.m, a.k) ? t : -1;
+  if (int(blockIdx.x) >= batch * ranges) {
+    const int64_t b = int64_t(blockIdx.x) - int64_t(batch) * ranges;
+    if (b < batch) tail_keys(a, b);
+    else attn_shares(a, int64_t(batch) * a.T, s_tmp);
+    return;
   }
-  hist[tid] = 0;
-  __syncthreads();
+  const int64_t b = blockIdx.x / ranges;
+  const int tid = threadIdx.x, lo = int(blockIdx.x % ranges) * kListNT;
   const int32_t* blocks = a.blocks + b * a.T * a.m;
   const int entries = a.T * a.m;
-  const int end = min(f, lo + kListNT);
-  // f(entry, block) for the entries of this range whose nodes need scores, eight loads in flight
+  constexpr int U = 8;
+  int first[U];  // this thread's first entries, loaded beside the lengths
+#pragma unroll
+  for (int u = 0; u < U; ++u) first[u] = tid + u * kListNT < entries ? blocks[tid + u * kListNT] : -1;
+  const int64_t c = a.ctx[b];
+  if (tid < a.T) {
+    const int t = a.rowpos[b * a.T + tid];
+    need[tid] = t >= 0 && candidates(t, a.B, a.m) > a.k;
+  }
+  hist[tid] = 0;
+  if (c < 0 || c >= a.capacity) return;
+  const int end = min(int(c / a.B), lo + kListNT);  // cached whole blocks of this range
+  __syncthreads();
+  // f(entry, block) for the entries of this range whose nodes need scores
   auto for_entries = [&](auto fn) {
-    for (int e0 = tid; e0 < entries; e0 += 8 * kListNT) {
-      int blk[8];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = e0 + u * kListNT;
-        blk[u] = e < entries ? blocks[e] : -1;
-      }
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int e = e0 + u * kListNT;
-        if (blk[u] >= lo && blk[u] < end && pos_s[e / a.m] >= 0) fn(e, blk[u]);
-      }
+    for (int u = 0; u < U; ++u) {
+      const int e = tid + u * kListNT;
+      if (first[u] >= lo && first[u] < end && need[e / a.m]) fn(e, first[u]);
+    }
+    for (int e = tid + U * kListNT; e < entries; e += kListNT) {
+      const int blk = blocks[e];
+      if (blk >= lo && blk < end && need[e / a.m]) fn(e, blk);
     }
   };
   for_entries([&](int, int blk) { atomicAdd(&hist[blk - lo], 1); });
-  // tail blocks: their keys, a warp per node, the nodes spread over the ranges
-  for (int i = range + warp * ranges; i < a.T; i += kListNT / 32 * ranges) {
-    const int t = pos_s[i];
-    if (t < 0) continue;
-    const int64_t row = b * a.T + i;
-    const int n = t - f * a.B + 1;  // tail rows of the node
-    const int nblk = min(a.m, t / a.B + 1);
-    const uint32_t* src = a.tailkeys + row * a.tail_ld;
-    for (int s = nblk - 1; s >= 0; --s) {
-      const int blk = blocks[i * a.m + s];
-      if (blk < f) break;
-      const int r0 = (blk - f) * a.B;
-      uint32_t* dst = a.tkeys + (row * a.m + s) * int64_t(a.B);
-      for (int r = lane; r < a.B && r0 + r < n; r += 32) dst[r] = src[r0 + r];
-    }
-  }
   __syncthreads();
-  // this range's items: `per` for each block with a pair
+  // this range's items, `per` for each block with a pair, and pairs: one scan of
+  // both counts (at most 512 blocks and 64 * 512 pairs)
   const int per = (a.B + 127) / 128;
   const int cnt = hist[tid];
-  int tot_p, tot_i;
-  const int at_p = block_exclusive_scan<kListNT>(cnt, s_tmp, &tot_p);
-  const int at_i = block_exclusive_scan<kListNT>(cnt > 0, s_tmp, &tot_i);
-  if (tot_p == 0) return;
-  if (tid == 0) s_base[0] = atomicAdd(a.counters, tot_i * per);
-  if (tid == 32) s_base[1] = atomicAdd(a.counters + 1, tot_p);
+  int total;
+  const int at = block_exclusive_scan<kListNT>(cnt | int(cnt > 0) << 20, s_tmp, &total);
+  const int at_p = at & 0xfffff, at_i = at >> 20;
+  if (total == 0) return;
+  if (tid == 0) s_base[0] = atomicAdd(a.counters, (total >> 20) * per);
+  if (tid == 32) s_base[1] = atomicAdd(a.counters + 1, total & 0xfffff);
   hist[tid] = at_p;
   __syncthreads();
   uint32_t* pairs = a.pairs + s_base[1];
   if (cnt)
     for (int ch = 0; ch < per; ++ch)
       a.items[s_base[0] + at_i * per + ch] =
-          make_int4(int(b * a.capacity) + mine * a.B + 128 * ch, s_base[1] + at_p,
+          make_int4(int(b * a.capacity) + (lo + tid) * a.B + 128 * ch, s_base[1] + at_p,
                     cnt | (min(128, a.B - 128 * ch) << 16), int(b << 3) | ch);
   for_entries([&](int e, int blk) {
     const int i = e / a.m;
@@ -199,8 +259,7 @@ __global__ void __launch_bounds__(NT) tree_topk_kernel(const TreeArgs a, int32_t
     for (int s = threadIdx.x; s < a.k; s += NT) out[s] = -1;
     return;
   }
-  const int64_t nb = t / a.B + 1;
-  const int n = int(nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1);
+  const int n = candidates(int(t), a.B, a.m);
   uint32_t key[KPT];
   if (n > a.k) load_keys<KPT>(a.tkeys + row * int64_t(a.m) * a.B, n, key);
   for (int s = threadIdx.x; s < a.m; s += NT) blk[s] = a.blocks[row * a.m + s];
@@ -237,12 +296,11 @@ __global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int64_
   const int64_t t = a.rowpos[row];
   if (t < 0) return;  // no part: its entries are -1
   const int c = a.ctx[row / a.T];
-  const int64_t nb = t / a.B + 1;
-  const int64_t n = min(int64_t(a.k), nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1);
+  const int n = min(a.k, candidates(int(t), a.B, a.m));
   const int32_t* path = a.paths + row * a.T;
   int32_t* out = idx + row * a.k;
-  for (int64_t e0 = n - 32; e0 > -32; e0 -= 32) {
-    const int64_t e = e0 + lane;
+  for (int e0 = n - 32; e0 > -32; e0 -= 32) {
+    const int e = e0 + lane;
     const int p = e >= 0 ? out[e] : -1;
     const bool late = p >= c;
     if (late) out[e] = c + min(max(path[min(p - c, a.T - 1)], 0), a.T - 1);
@@ -261,8 +319,7 @@ __device__ void attend_row(const TreeArgs& a, int64_t row, const uint16_t* Q, co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t b = row / a.T, base = b * a.capacity;
   const int64_t t = a.rowpos[row];
-  const int64_t nb = t / a.B + 1;
-  const int n = int(min(int64_t(a.k), nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1));
+  const int n = min(a.k, candidates(int(t), a.B, a.m));
   for (int h = h0 + warp; h < h1; h += 8) {
     const uint4* q = reinterpret_cast<const uint4*>(Q + (row * H + h) * D);
     float M = -INFINITY, l = 0.f, o[V] = {};
@@ -494,7 +551,7 @@ void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, co
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s) {
   const int ranges = int((a.capacity / a.B + kListNT - 1) / kListNT);
   count_launches(1);
-  launch_kernel(true, tree_lists_kernel, unsigned(batch * ranges), kListNT, 0, s, a, ranges);
+  launch_kernel(true, tree_lists_kernel, unsigned(batch * (ranges + 1) + 1), kListNT, 0, s, a, batch, ranges);
 }
 
 void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStream_t s) {

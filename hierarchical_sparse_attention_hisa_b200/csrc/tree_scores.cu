@@ -91,53 +91,6 @@ HSA_DEV float dot8(const uint4& kv, const float (&q)[8]) {
   return acc;
 }
 
-// The attention's work: all rows' 128-key tiles, in row order, cut into
-// kTreeAttnCtas equal shares (what a row keeps follows from its position
-// alone). A row per CTA leaves most SMs idle when trees are ragged; with equal
-// shares at most two rows of a CTA are cut, whose parts are combined.
-__device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
-  const int tid = threadIdx.x;
-  auto kept_of = [&](int64_t row) -> int {
-    const int64_t t = row < rows ? node_position(a, row / a.T, int(row % a.T)) : -1;
-    if (t < 0) return 0;
-    const int64_t nb = t / a.B + 1;
-    const int64_t n = nb <= a.m ? t + 1 : int64_t(a.m - 1) * a.B + t % a.B + 1;
-    return int(min(n, int64_t(a.k)));
-  };
-  int64_t total = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += kNT) {
-    int sum;
-    block_exclusive_scan<kNT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
-    total += sum;
-  }
-  const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
-  int64_t tile0 = 0;
-  int item0 = 0, part0 = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += kNT) {
-    const int64_t row = r0 + tid;
-    const int kept = kept_of(row), n = (kept + 127) / 128;
-    int sum, items, parts;
-    const int64_t s = tile0 + block_exclusive_scan<kNT>(n, s_tmp, &sum);
-    const int64_t c0 = s / quota;
-    const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
-    int at = item0 + block_exclusive_scan<kNT>(pieces, s_tmp, &items);
-    const int part = part0 + block_exclusive_scan<kNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
-    if (row < rows) {
-      a.row_parts[row] = make_int2(part, pieces);
-      a.flags[row] = 0;
-    }
-    for (int j = 0; j < pieces; ++j, ++at) {
-      const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
-      a.attn_items[at] = make_int4(int(row), int(lo - s) | int(hi - lo) << 8 | kept << 16, pieces > 1 ? part + j : -1, 0);
-      if (lo == (c0 + j) * quota) a.cta_items[c0 + j] = at;  // the first item of CTA c0 + j
-    }
-    tile0 += sum;
-    item0 += items;
-    part0 += parts;
-  }
-  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += kNT) a.cta_items[c] = item0;
-}
-
 // tid: 0 .. kNodeNT-1 within the node's warps; bar: their named barrier; sc: tail_ld floats
 template <int DI>
 __device__ void node_tail(const TreeArgs& a, int64_t b, int i, int tid, int bar, float* sc) {
@@ -162,7 +115,7 @@ __device__ void node_tail(const TreeArgs& a, int64_t b, int i, int tid, int bar,
   }
   const int64_t nb = t / a.B + 1;
   const int64_t f = c / a.B;
-  const bool tokens = needs_scores(t, a.B, a.m, a.k);
+  const bool tokens = candidates(int(t), a.B, a.m) > a.k;  // else all are kept, without scores
   const bool blocks = nb > a.m && f < nb - 1;  // whole blocks in the tail
   if (!tokens && !blocks) return;
   // tail rows: cached ones from f*B, then the path
@@ -319,18 +272,12 @@ __device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint
 }
 
 template <int DI>
-__global__ void __launch_bounds__(kNT) tree_tails_kernel(const TreeArgs a, int64_t rows) {
+__global__ void __launch_bounds__(kNT) tree_tails_kernel(const TreeArgs a) {
   extern __shared__ __align__(16) float tail_smem[];
-  __shared__ int s_tmp[kNT / 32 + 1];
   griddep_wait();
   griddep_launch();
-  if (blockIdx.y == gridDim.y - 1) {  // one CTA more: the lists' counters, the attention's shares
-    if (blockIdx.x > 0) return;
-    if (threadIdx.x < 2) a.counters[threadIdx.x] = 0;
-    attn_shares(a, rows, s_tmp);
-    return;
-  }
   const int64_t b = blockIdx.x;
+  if (b == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
   const int half = threadIdx.x / kNodeNT, i = int(blockIdx.y) * kNodesPerCta + half;
   if (i < a.T) node_tail<DI>(a, b, i, threadIdx.x % kNodeNT, 1 + half, tail_smem + half * a.tail_ld);
 }
@@ -531,8 +478,8 @@ bool launch_bs(const TreeArgs& a, int batch, cudaStream_t s) {
   auto blocks = tree_block_scores_kernel<DI, N>;
   if (cudaFuncSetAttribute(blocks, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_b) != cudaSuccess) return false;
   count_launches(2);
-  launch_kernel(true, tree_tails_kernel<DI>, dim3(unsigned(batch), unsigned((a.T + kNodesPerCta - 1) / kNodesPerCta + 1)),
-                kNT, size_t(smem_t), s, a, int64_t(batch) * a.T);
+  launch_kernel(true, tree_tails_kernel<DI>, dim3(unsigned(batch), unsigned((a.T + kNodesPerCta - 1) / kNodesPerCta)),
+                kNT, size_t(smem_t), s, a);
   launch_kernel(true, blocks, dim3(unsigned(batch), unsigned(tiles)), kNT, size_t(smem_b), s, a);
   return true;
 }
