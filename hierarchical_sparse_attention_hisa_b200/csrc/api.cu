@@ -446,9 +446,9 @@ namespace {
 //   keys [rows][tail_ld] u32, kept blocks [rows][m] i32, pairs [rows][m] u32,
 //   items [max_items] int4, token-score keys [rows][m*B] u32, indices [rows][k]
 //   i32 (unless the caller takes them), the attention's items, their CTAs' first
-//   ones, the rows' parts and flags, and the parts: O f32, maxima and row sums f32.
+//   ones, the rows that are cut, the rows' flags, and the parts: O f32, maxima and row sums f32.
 struct TreeWs {
-  size_t counters, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, aitems, cta, rparts, flags, opart, mpart, lpart,
+  size_t counters, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, aitems, cta, cut, flags, opart, mpart, lpart,
       total;
   int64_t rows, ldb, max_items;
   int tail_ld;
@@ -476,7 +476,7 @@ TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) 
   const size_t parts = 2 * hsa::kTreeAttnCtas;
   w.aitems = take((rows + hsa::kTreeAttnCtas) * 16);
   w.cta = take((hsa::kTreeAttnCtas + 1) * 4);
-  w.rparts = take(rows * 8);
+  w.cut = take(hsa::kTreeAttnCtas * 16);
   w.flags = take(rows * 4);
   w.opart = take(parts * p->H * p->d * 4);
   w.mpart = take(parts * p->H * 4);
@@ -558,7 +558,8 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   a.counters = reinterpret_cast<int*>(ws + w.counters);
   a.attn_items = reinterpret_cast<int4*>(ws + w.aitems);
   a.cta_items = reinterpret_cast<int*>(ws + w.cta);
-  a.row_parts = reinterpret_cast<int2*>(ws + w.rparts);
+  a.cut = reinterpret_cast<int4*>(ws + w.cut);
+  a.O = O; a.H = p->H;
   a.flags = reinterpret_cast<int*>(ws + w.flags);
   // The kernels are programmatic dependent launches, as in a decode step.
   // 1. drafted rows appended, tails and cached blocks scored; top-m
@@ -579,8 +580,8 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   float* opart = reinterpret_cast<float*>(ws + w.opart);
   float* mpart = reinterpret_cast<float*>(ws + w.mpart);
   float* lpart = reinterpret_cast<float*>(ws + w.lpart);
-  if (!hsa::launch_tree_attn(a, Q_new, idx, p->H, softmax_scale(p), O, opart, mpart, lpart, stream)) return HSA_ERR_CUDA;
-  hsa::launch_tree_combine(a, w.rows, Q_new, idx, p->H, softmax_scale(p), opart, mpart, lpart, O, stream);
+  if (!hsa::launch_tree_attn(a, Q_new, idx, softmax_scale(p), opart, mpart, lpart, stream)) return HSA_ERR_CUDA;
+  hsa::launch_tree_combine(a, w.rows, Q_new, idx, softmax_scale(p), opart, mpart, lpart, stream);
   return launch_status();
 }
 

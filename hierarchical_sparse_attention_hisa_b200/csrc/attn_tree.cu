@@ -519,21 +519,21 @@ bool launch_d(const Args& a, cudaStream_t s) {
 
 }  // namespace
 
-bool launch_tree_attn(const TreeArgs& t, const void* Q, const int32_t* idx, int H, float scale, void* O, float* Opart,
-                      float* mpart, float* lpart, cudaStream_t s) {
+bool launch_tree_attn(const TreeArgs& t, const void* Q, const int32_t* idx, float scale, float* Opart, float* mpart,
+                      float* lpart, cudaStream_t s) {
   Args a{};
   a.Q = static_cast<const uint16_t*>(Q);
   a.K = t.K_cache; a.V = t.V_cache;
-  a.idx = idx; a.T = t.T; a.k = t.k; a.H = H;
+  a.idx = idx; a.T = t.T; a.k = t.k; a.H = t.H;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.capacity = t.capacity;
   a.items = t.attn_items; a.cta_items = t.cta_items;
-  a.O = static_cast<uint16_t*>(O);
+  a.O = t.O;
   a.Opart = Opart; a.mpart = mpart; a.lpart = lpart;
   a.flags = t.flags;
-  for (int h0 = 0; h0 < H; h0 += 64) {
+  for (int h0 = 0; h0 < t.H; h0 += 64) {
     a.h0 = h0;
-    a.nh = H - h0 < 64 ? H - h0 : 64;
+    a.nh = t.H - h0 < 64 ? t.H - h0 : 64;
     if (!(t.d == 128 ? launch_d<128>(a, s) : launch_d<64>(a, s))) return false;
   }
   return true;

@@ -99,12 +99,14 @@ struct TreeArgs {
   int4* items;                     // (first key row, first pair, pairs | key rows << 16, sequence << 3 | 128-row piece)
   int* counters;                   // [2]: items, pairs
   // the attention's work: items (row, first tile | tiles << 8 | kept rows << 16, part or -1 to write O whole, -)
-  // and each CTA's first; of each row its first part and how many (0: nothing kept, 1: written whole), and
-  // whether its weights left the range of the first pass
+  // and each CTA's first; the rows that lie in several CTAs (row, first part, parts, -); and of each row whether
+  // its weights left the range of the fixed reference
   int4* attn_items;
   int* cta_items;                  // [kTreeAttnCtas + 1]
-  int2* row_parts;                 // [rows]
+  int4* cut;                       // [kTreeAttnCtas], row -1 behind the last
   int* flags;                      // [rows]
+  uint16_t* O;                     // [rows][H][d]
+  int H;
 };
 constexpr int kTreeAttnCtas = 148;  // one per SM
 constexpr int kBkeys0 = 3;          // so that block 1's key, the first candidate, is on 16 bytes
@@ -113,7 +115,7 @@ constexpr int kWideRows = 592;      // two CTAs of 1024 threads per SM, two wave
 HSA_DEV int candidates(int t, int B, int m) { return t / B < m ? t + 1 : (m - 1) * B + t % B + 1; }
 void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, const int32_t* n_nodes,
                       const int32_t* parents, int32_t* positions, int32_t* paths, cudaStream_t s);
-// (also appends the drafted rows to the caches and scores every node's tail)
+// (also appends the drafted rows to the caches, scores every node's tail, and zeroes the O of nodes that take no part)
 bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStream_t s);
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s);
 bool launch_tree_token_scores(const TreeArgs& a, int batch, int d_idx, int64_t max_items, cudaStream_t s);
@@ -122,10 +124,10 @@ void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStre
 bool tree_topk_wide(const TreeArgs& a, int64_t rows);
 void launch_tree_topk(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s);
 void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s);
-bool launch_tree_attn(const TreeArgs& t, const void* Q, const int32_t* idx, int H, float scale, void* O, float* Opart,
-                      float* mpart, float* lpart, cudaStream_t s);
-void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const int32_t* idx, int H, float scale,
-                         const float* Opart, const float* mpart, const float* lpart, void* O, cudaStream_t s);
+bool launch_tree_attn(const TreeArgs& t, const void* Q, const int32_t* idx, float scale, float* Opart, float* mpart,
+                      float* lpart, cudaStream_t s);
+void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const int32_t* idx, float scale,
+                         const float* Opart, const float* mpart, const float* lpart, cudaStream_t s);
 int tree_attn_wait_flag(bool reset);
 bool tree_attn_set_inject(bool on);
 void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(256) tree_plan_kernel(int T, int64_t capacity,
 // 128 rows of such a block. The order of items and of pairs inside one is not
 // fixed (atomics); each writes its own keys, so results do not depend on it.
 //
-// Beside them, a CTA per sequence gives the kept tail blocks their keys from the
+// Beside them, a warp per node gives the kept tail blocks their keys from the
 // tail's scores, and one CTA cuts the attention's work.
 // ---------------------------------------------------------------------------
 constexpr int kListNT = 512;
@@ -89,20 +89,19 @@ __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
   }
   const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
   int64_t tile0 = 0;
-  int item0 = 0, part0 = 0;
+  int item0 = 0, part0 = 0, cut0 = 0;
   for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
     const int64_t row = r0 + tid;
     const int kept = kept_of(row), n = (kept + 127) / 128;
-    int sum, items, parts;
+    int sum, items, parts, cuts;
     const int64_t s = tile0 + block_exclusive_scan<kListNT>(n, s_tmp, &sum);
     const int64_t c0 = s / quota;
     const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
     int at = item0 + block_exclusive_scan<kListNT>(pieces, s_tmp, &items);
     const int part = part0 + block_exclusive_scan<kListNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
-    if (row < rows) {
-      a.row_parts[row] = make_int2(part, pieces);
-      a.flags[row] = 0;
-    }
+    const int ncut = cut0 + block_exclusive_scan<kListNT>(pieces > 1, s_tmp, &cuts);
+    if (row < rows) a.flags[row] = 0;
+    if (pieces > 1) a.cut[ncut] = make_int4(int(row), part, pieces, 0);
     for (int j = 0; j < pieces; ++j, ++at) {
       const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
       a.attn_items[at] = make_int4(int(row), int(lo - s) | int(hi - lo) << 8 | kept << 16, pieces > 1 ? part + j : -1, 0);
@@ -111,32 +110,30 @@ __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
     tile0 += sum;
     item0 += items;
     part0 += parts;
+    cut0 += cuts;
   }
   for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += kListNT) a.cta_items[c] = item0;
+  // (a cut lies between two CTAs, so fewer rows than CTAs are cut)
+  for (int c = cut0 + tid; c < kTreeAttnCtas; c += kListNT) a.cut[c] = make_int4(-1, 0, 0, 0);
 }
 
-__device__ void tail_keys(const TreeArgs& a, int64_t b) {
-  const int64_t c = a.ctx[b];
-  if (c < 0 || c >= a.capacity) return;
+__device__ void tail_keys(const TreeArgs& a, int64_t row) {  // a warp per node
+  const int64_t c = a.ctx[row / a.T];
+  const int t = a.rowpos[row];
+  if (t < 0 || candidates(t, a.B, a.m) <= a.k) return;
   const int f = int(c / a.B), lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < a.T; i += kListNT / 32) {  // a warp per node
-    const int64_t row = b * a.T + i;
-    const int t = a.rowpos[row];
-    if (t < 0 || candidates(t, a.B, a.m) <= a.k) continue;
-    const int nb = t / a.B + 1, n = t - f * a.B + 1;  // n: the node's tail rows
-    const int nblk = min(a.m, nb);
-    const uint32_t* src = a.tailkeys + row * a.tail_ld;
-    // the kept tail blocks are the last of the list, 32 looked up at a time
-    for (int s0 = nblk - 1; s0 >= 0; s0 -= 32) {
-      const int mine = s0 - lane >= 0 ? a.blocks[row * a.m + s0 - lane] : -1;
-      const int cnt = __popc(__ballot_sync(kFull, mine >= f));
-      for (int u = 0; u < cnt; ++u) {
-        const int r0 = (__shfl_sync(kFull, mine, u) - f) * a.B;
-        uint32_t* dst = a.tkeys + (row * a.m + s0 - u) * int64_t(a.B);
-        for (int r = lane; r < a.B && r0 + r < n; r += 32) dst[r] = src[r0 + r];
-      }
-      if (cnt < 32) break;
+  const int n = t - f * a.B + 1;  // the node's tail rows
+  const uint32_t* src = a.tailkeys + row * a.tail_ld;
+  // the kept tail blocks are the last of the list, 32 looked up at a time
+  for (int s0 = min(a.m, t / a.B + 1) - 1; s0 >= 0; s0 -= 32) {
+    const int mine = s0 - lane >= 0 ? a.blocks[row * a.m + s0 - lane] : -1;
+    const int cnt = __popc(__ballot_sync(kFull, mine >= f));
+    for (int u = 0; u < cnt; ++u) {
+      const int r0 = (__shfl_sync(kFull, mine, u) - f) * a.B;
+      uint32_t* dst = a.tkeys + (row * a.m + s0 - u) * int64_t(a.B);
+      for (int r = lane; r < a.B && r0 + r < n; r += 32) dst[r] = src[r0 + r];
     }
+    if (cnt < 32) break;
   }
 }
 
@@ -147,10 +144,13 @@ __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, i
   __shared__ uint8_t need[kTreeMax];
   griddep_wait();
   griddep_launch();
+  if (blockIdx.x == gridDim.x - 1) {
+    attn_shares(a, int64_t(batch) * a.T, s_tmp);
+    return;
+  }
   if (int(blockIdx.x) >= batch * ranges) {
-    const int64_t b = int64_t(blockIdx.x) - int64_t(batch) * ranges;
-    if (b < batch) tail_keys(a, b);
-    else attn_shares(a, int64_t(batch) * a.T, s_tmp);
+    const int64_t row = (int64_t(blockIdx.x) - int64_t(batch) * ranges) * (kListNT / 32) + (threadIdx.x >> 5);
+    if (row < int64_t(batch) * a.T) tail_keys(a, row);
     return;
   }
   const int64_t b = blockIdx.x / ranges;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(NT) tree_topm_kernel(const TreeArgs a, int32_t
 // Top-k of a node's candidates (the tokens of its kept blocks, ascending), and
 // their positions as rows of the sequence's cache.
 template <int NT, int KPT>
-__global__ void __launch_bounds__(NT) tree_topk_kernel(const TreeArgs a, int32_t* __restrict__ idx) {
+__global__ void __launch_bounds__(NT, NT == 1024 && KPT <= 8 ? 2 : 1) tree_topk_kernel(const TreeArgs a, int32_t* __restrict__ idx) {
   __shared__ uint32_t hist[RegSelect<NT, KPT>::kBins];
   __shared__ int scratch[NT / 32 + 8];
   __shared__ int blk[512];
@@ -308,124 +308,110 @@ __global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int64_
   }
 }
 
-// The softmax of one row whose weights left the range that the attention's
-// fixed reference covers, on CUDA cores with a running maximum: a warp per head
-// (HPC heads per CTA), 128 kept rows at a time. A lane scores four rows, then
-// holds D / 32 output values.
+// One head of a row whose weights left the range that the attention's fixed
+// reference covers, on CUDA cores with a running maximum, by a warp: 128 kept
+// rows at a time, a lane scores four of them, then holds D / 32 output values.
+// (Out of line: the registers it needs would halve the CTAs of the combination.)
 template <int D>
-__device__ void attend_row(const TreeArgs& a, int64_t row, const uint16_t* Q, const int32_t* idx, int H, int h0, int h1,
-                           float scale, float (*p_s)[128], uint16_t* O) {
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = row / a.T, base = b * a.capacity;
-  const int64_t t = a.rowpos[row];
-  const int n = min(a.k, candidates(int(t), a.B, a.m));
-  for (int h = h0 + warp; h < h1; h += 8) {
-    const uint4* q = reinterpret_cast<const uint4*>(Q + (row * H + h) * D);
-    float M = -INFINITY, l = 0.f, o[V] = {};
-    for (int c0 = 0; c0 < n; c0 += 128) {
-      float x[4], top = -INFINITY;
-      bool bad = false;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + 32 * u + lane;
-        x[u] = -INFINITY;
-        if (c < n) {
-          const uint4* kr = reinterpret_cast<const uint4*>(a.K_cache + (base + max(idx[row * a.k + c], 0)) * D);
-          float acc = 0.f;
-          for (int e = 0; e < D / 8; ++e) {
-            const uint4 kv = kr[e], qv = __ldg(q + e);
-            acc = __fmaf_rn(bf16_lo(qv.x), bf16_lo(kv.x), acc); acc = __fmaf_rn(bf16_hi(qv.x), bf16_hi(kv.x), acc);
-            acc = __fmaf_rn(bf16_lo(qv.y), bf16_lo(kv.y), acc); acc = __fmaf_rn(bf16_hi(qv.y), bf16_hi(kv.y), acc);
-            acc = __fmaf_rn(bf16_lo(qv.z), bf16_lo(kv.z), acc); acc = __fmaf_rn(bf16_hi(qv.z), bf16_hi(kv.z), acc);
-            acc = __fmaf_rn(bf16_lo(qv.w), bf16_lo(kv.w), acc); acc = __fmaf_rn(bf16_hi(qv.w), bf16_hi(kv.w), acc);
-          }
-          x[u] = acc * scale;
-          bad = bad || x[u] != x[u];
+__device__ __noinline__ void attend_head(const uint16_t* K, const uint16_t* V, const int32_t* idx, int n,
+                                         const uint16_t* q, float scale, float* p_s, uint16_t* out) {
+  constexpr int VPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  float M = -INFINITY, l = 0.f, o[VPL] = {};
+  for (int c0 = 0; c0 < n; c0 += 128) {
+    float x[4], top = -INFINITY;
+    bool bad = false;
+#pragma unroll 1
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + 32 * u + lane;
+      float acc = -INFINITY;
+      if (c < n) {
+        const uint4* kr = reinterpret_cast<const uint4*>(K + int64_t(max(idx[c], 0)) * D);
+        const uint4* qr = reinterpret_cast<const uint4*>(q);
+        acc = 0.f;
+#pragma unroll 2
+        for (int e = 0; e < D / 8; ++e) {
+          const uint4 kv = kr[e], qv = qr[e];
+          acc = __fmaf_rn(bf16_lo(qv.x), bf16_lo(kv.x), acc); acc = __fmaf_rn(bf16_hi(qv.x), bf16_hi(kv.x), acc);
+          acc = __fmaf_rn(bf16_lo(qv.y), bf16_lo(kv.y), acc); acc = __fmaf_rn(bf16_hi(qv.y), bf16_hi(kv.y), acc);
+          acc = __fmaf_rn(bf16_lo(qv.z), bf16_lo(kv.z), acc); acc = __fmaf_rn(bf16_hi(qv.z), bf16_hi(kv.z), acc);
+          acc = __fmaf_rn(bf16_lo(qv.w), bf16_lo(kv.w), acc); acc = __fmaf_rn(bf16_hi(qv.w), bf16_hi(kv.w), acc);
         }
-        top = fmaxf(top, x[u]);
+        acc *= scale;
+        bad = bad || acc != acc;
       }
-#pragma unroll
-      for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
-      const float Mn = fmaxf(M, top), ref = Mn == -INFINITY ? 0.f : Mn;
-      const float g = M == -INFINITY ? 0.f : expf(M - ref);
-      float add = bad ? NAN : 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float p = expf(x[u] - ref);
-        add += p;
-        p_s[warp][32 * u + lane] = p;
-      }
-#pragma unroll
-      for (int s = 16; s >= 1; s >>= 1) add += __shfl_xor_sync(kFull, add, s);
-      l = l * g + add;
-      M = Mn;
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[e] *= g;
-      __syncwarp();
-      for (int c = c0; c < min(n, c0 + 128); ++c) {
-        const float p = p_s[warp][c - c0];
-        const uint16_t* vr = a.V_cache + (base + max(idx[row * a.k + c], 0)) * D + lane * V;
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = __fmaf_rn(p, __uint_as_float(uint32_t(vr[e]) << 16), o[e]);
-      }
-      __syncwarp();
+      p_s[32 * u + lane] = acc;
+      top = fmaxf(top, acc);
     }
-    // (every score -inf: no weights at all, as a row that keeps nothing)
-    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-    for (int e = 0; e < V; ++e) O[(row * H + h) * D + lane * V + e] = uint16_t(f32_to_bf16_rn(o[e] * inv));
+    for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
+    const float Mn = fmaxf(M, top), ref = Mn == -INFINITY ? 0.f : Mn;
+    const float g = M == -INFINITY ? 0.f : expf(M - ref);
+    float add = bad ? NAN : 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      x[u] = expf(p_s[32 * u + lane] - ref);
+      add += x[u];
+      p_s[32 * u + lane] = x[u];
+    }
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) add += __shfl_xor_sync(kFull, add, s);
+    l = l * g + add;
+    M = Mn;
+#pragma unroll
+    for (int e = 0; e < VPL; ++e) o[e] *= g;
+    __syncwarp();
+#pragma unroll 1
+    for (int c = c0; c < min(n, c0 + 128); ++c) {
+      const float p = p_s[c - c0];
+      const uint16_t* vr = V + int64_t(max(idx[c], 0)) * D + lane * VPL;
+#pragma unroll
+      for (int e = 0; e < VPL; ++e) o[e] = __fmaf_rn(p, __uint_as_float(uint32_t(vr[e]) << 16), o[e]);
+    }
+    __syncwarp();
   }
+  // (every score -inf: no weights at all, as a row that keeps nothing)
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int e = 0; e < VPL; ++e) out[lane * VPL + e] = uint16_t(f32_to_bf16_rn(o[e] * inv));
 }
 
 // O of the rows that were cut (with M the largest part maximum, O = sum_p
-// 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), of the rows that keep
-// nothing (zero), and of the flagged ones (taken again). Grid (rows / 4, head
-// groups), a thread per four values; the parts come eight at a time, every load
-// of a group issued before any is used. Most rows of a large call were written
-// whole: a CTA looks four up at once (one each: 4096 CTAs, 12 us for 512 rows).
-constexpr int kCombineRows = 4;
-template <int D>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int64_t rows, int rows_per_cta,
-                                                           const uint16_t* __restrict__ Q,
-                                                           const int32_t* __restrict__ idx, int H, float scale,
-                                                           const float* __restrict__ Opart,
-                                                           const float* __restrict__ mpart,
-                                                           const float* __restrict__ lpart, uint16_t* __restrict__ O) {
-  constexpr int TPH = D / 4, HPC = 256 / TPH, U = 8;  // threads per head, heads per CTA at a time
+// 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), and of the flagged
+// rows (taken again). Grid (cut, head groups), a thread per four values; the
+// parts come U at a time, every load of a group issued before any is used.
+template <int D, int U>
+__global__ void __launch_bounds__(256, U == 4 ? 6 : 4) tree_combine_kernel(const TreeArgs a, int64_t rows,
+                                                                          const uint16_t* __restrict__ Q,
+                                                                          const int32_t* __restrict__ idx, float scale,
+                                                                          const float* __restrict__ Opart,
+                                                                          const float* __restrict__ mpart,
+                                                                          const float* __restrict__ lpart) {
+  constexpr int TPH = D / 4, HPC = 256 / TPH;  // threads per head, heads per CTA at a time
   __shared__ float p_s[8][128];
   griddep_wait();
   griddep_launch();
-  const int v = threadIdx.x % TPH;
-  int2 parts[kCombineRows];
-  int flag[kCombineRows];
-#pragma unroll
-  for (int i = 0; i < kCombineRows; ++i) {
-    const int64_t row = int64_t(blockIdx.x) * rows_per_cta + i;
-    const bool in = i < rows_per_cta && row < rows;
-    parts[i] = in ? a.row_parts[row] : make_int2(0, 1);
-    flag[i] = in ? a.flags[row] : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < kCombineRows; ++i) {
-  const int64_t row = int64_t(blockIdx.x) * rows_per_cta + i;
-  const int2 rp = parts[i];
-  if (flag[i]) {
-    for (int h = blockIdx.y * HPC; h < H; h += gridDim.y * HPC)
-      attend_row<D>(a, row, Q, idx, H, h, min(H, h + HPC), scale, p_s, O);
-    continue;
-  }
-  if (rp.y == 1) continue;  // written whole
+  const int H = a.H, v = threadIdx.x % TPH;
+  const int4 cut = a.cut[blockIdx.x];
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+    if (a.flags[row]) {
+      const int64_t base = row / a.T * a.capacity * D;
+      const int n = min(a.k, candidates(a.rowpos[row], a.B, a.m));
+      for (int h = blockIdx.y * 8 + threadIdx.x / 32; h < H; h += gridDim.y * 8)
+        attend_head<D>(a.K_cache + base, a.V_cache + base, idx + row * a.k, n, Q + (row * H + h) * D, scale,
+                       p_s[threadIdx.x / 32], a.O + (row * H + h) * D);
+    }
+  if (cut.x < 0 || a.flags[cut.x]) return;
   for (int h = blockIdx.y * HPC + threadIdx.x / TPH; h < H; h += gridDim.y * HPC) {
     float M = -INFINITY, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int p0 = 0; p0 < rp.y; p0 += U) {
+    for (int p0 = 0; p0 < cut.z; p0 += U) {
       float l[U], m[U];
       float4 o[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const bool in = p0 + u < rp.y;
-        const int64_t w = int64_t(rp.x + p0 + u) * H + h;
+        const bool in = p0 + u < cut.z;
+        const int64_t w = int64_t(cut.y + p0 + u) * H + h;
         l[u] = in ? lpart[w] : 0.f;
         m[u] = in ? mpart[w] : -INFINITY;
         o[u] = in ? reinterpret_cast<const float4*>(Opart + w * D)[v] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -445,10 +431,9 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeArgs a, int
         den = __fmaf_rn(f, l[u], den);
       }
     }
-    const float inv = den > 0.f ? 1.f / den : 0.f;
-    reinterpret_cast<uint2*>(O + (row * H + h) * D)[v] =
+    const float inv = 1.f / den;
+    reinterpret_cast<uint2*>(a.O + (int64_t(cut.x) * H + h) * D)[v] =
         make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
-  }
   }
 }
 
@@ -551,7 +536,8 @@ void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, co
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s) {
   const int ranges = int((a.capacity / a.B + kListNT - 1) / kListNT);
   count_launches(1);
-  launch_kernel(true, tree_lists_kernel, unsigned(batch * (ranges + 1) + 1), kListNT, 0, s, a, batch, ranges);
+  const unsigned tails = unsigned((int64_t(batch) * a.T + kListNT / 32 - 1) / (kListNT / 32));
+  launch_kernel(true, tree_lists_kernel, unsigned(batch * ranges) + tails + 1, kListNT, 0, s, a, batch, ranges);
 }
 
 void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStream_t s) {
@@ -584,16 +570,14 @@ void launch_tree_rows(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_
   launch_kernel(true, tree_rows_kernel, unsigned((rows + 7) / 8), 256, 0, s, a, rows, idx);
 }
 
-void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const int32_t* idx, int H, float scale,
-                         const float* Opart, const float* mpart, const float* lpart, void* O, cudaStream_t s) {
-  // a CTA per head group, fewer when the rows alone make a large grid
-  const int per = rows > 2 * num_sms() ? kCombineRows : 1;
-  const int64_t ctas = (rows + per - 1) / per;
-  const int64_t groups = std::min<int64_t>((H * a.d + 1023) / 1024, std::max<int64_t>(1, 8192 / ctas));
-  const dim3 grid{unsigned(ctas), unsigned(groups)};
+void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const int32_t* idx, float scale,
+                         const float* Opart, const float* mpart, const float* lpart, cudaStream_t s) {
+  const dim3 grid{unsigned(kTreeAttnCtas), unsigned((a.H * a.d + 1023) / 1024)};
   count_launches(1);
-  launch_kernel(true, a.d == 128 ? tree_combine_kernel<128> : tree_combine_kernel<64>, grid, 256, 0, s, a, rows, per,
-                (const uint16_t*)Q, idx, H, scale, Opart, mpart, lpart, (uint16_t*)O);
+  // few rows are cut into many parts, many rows into two: there fewer registers put the grid into one wave
+  auto kern = rows <= 64 ? (a.d == 128 ? tree_combine_kernel<128, 8> : tree_combine_kernel<64, 8>)
+                         : (a.d == 128 ? tree_combine_kernel<128, 4> : tree_combine_kernel<64, 4>);
+  launch_kernel(true, kern, grid, 256, 0, s, a, rows, (const uint16_t*)Q, idx, scale, Opart, mpart, lpart);
 }
 
 void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,

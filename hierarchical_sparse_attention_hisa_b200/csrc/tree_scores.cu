@@ -98,7 +98,11 @@ __device__ void node_tail(const TreeArgs& a, int64_t b, int i, int tid, int bar,
   const int64_t c = a.ctx[b];
   const int64_t t = node_position(a, b, i);
   if (tid == 0) a.rowpos[row] = int32_t(t);
-  if (t < 0) return;
+  if (t < 0) {
+    uint4* o = reinterpret_cast<uint4*>(a.O + row * a.H * a.d);
+    for (int e = tid; e < a.H * a.d / 8; e += kNodeNT) o[e] = make_uint4(0, 0, 0, 0);
+    return;
+  }
   const int lane = tid & 31, warp = tid >> 5;
   {  // the drafted rows, node i in cache row c + i
     const int64_t at = b * a.capacity + c + i;
