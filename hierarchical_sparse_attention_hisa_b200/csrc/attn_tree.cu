@@ -126,10 +126,11 @@ HSA_DEV void wait_warp(uint64_t* bar, uint32_t parity, bool& dead) {
   dead = !__all_sync(kFull, ok);
 }
 
-// Sum of v[0..N) over the 32 lanes by halving exchanges: lane l ends with the
-// sum of element l / (32 / N) (N <= 32, a power of two).
-template <int N>
+// Sum (or maximum) of v[0..N) over the 32 lanes by halving exchanges: lane l ends
+// with that of element l / (32 / N) (N <= 32, a power of two).
+template <int N, bool MAX = false>
 HSA_DEV float lanes_sum(float (&v)[N]) {
+  auto join = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
   const int lane = threadIdx.x & 31;
   int n = N;
 #pragma unroll
@@ -141,19 +142,13 @@ HSA_DEV float lanes_sum(float (&v)[N]) {
       for (int i = 0; i < N / 2; ++i)
         if (i < n) {
           const float send = hi ? v[i] : v[i + n], keep = hi ? v[i + n] : v[i];
-          v[i] = keep + __shfl_xor_sync(kFull, send, o);
+          v[i] = join(keep, __shfl_xor_sync(kFull, send, o));
         }
     } else {
-      v[0] += __shfl_xor_sync(kFull, v[0], o);
+      v[0] = join(v[0], __shfl_xor_sync(kFull, v[0], o));
     }
   }
   return v[0];
-}
-
-HSA_DEV float redux_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
 }
 
 struct Item { int row, t0, nt, kept, part; };
@@ -379,10 +374,9 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
             float x[CW];
             load_cols(sb * HP + h0 + c, x);
 #pragma unroll
-            for (int e = 0; e < CW; ++e) {
-              const float wm = redux_max(valid ? x[e] * a.scale_log2 : -INFINITY);
-              if (lane == e) red[sg][quad][h0 + c + e] = wm;
-            }
+            for (int e = 0; e < CW; ++e) x[e] = valid ? x[e] * a.scale_log2 : -INFINITY;
+            const float m = lanes_sum<CW, true>(x);
+            if (lane % (32 / CW) == 0) red[sg][quad][h0 + c + lane / (32 / CW)] = m;
           }
           bar_sync(half_bar, 128);
           if (quad == 0 && lane < HPT) {
