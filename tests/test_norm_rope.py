@@ -3,13 +3,13 @@ and interleaved rotations, far and negative positions, in-place calls; and
 the refusals (on the CPU).
 
 Tolerance. The result is rounded once to bf16: half a step, 2^-8 of the value.
-Before that, with y the normed row (ymax its largest magnitude): the sum of
-squares, the reciprocal root and the two products are off by at most 16 steps
-of 2^-24 relative; the angle, held as a fraction of a turn in fp32, by 2^-25
-turns = 2^-25 * 2 pi < 2^-22 radians, the sine and cosine by another 2^-23, and
-the rotation's three roundings by 3 * 2^-24 of |a| + |b| <= 2 ymax. Together
-less than 2 ymax (16 + 4 + 2 + 3) 2^-24 < 4e-6 ymax, and the rounding's half
-step is taken of a value that may be off by that much.
+Before that, with y the normed row (ymax its largest magnitude), in units of
+2^-24: the sum of squares, the reciprocal root and the products with it and the
+weight are off by at most 16 relative; the angle, 2^-32 of a turn and its
+conversion to fp32, by 2^-22.3 radians (3.2); the fast sine and cosine by 2^-21.2
+in [-pi, pi] (7); the coefficients and the rotation round five times (5). All of
+it is relative to |a| + |b| <= 2 ymax: 2 ymax * 31.2 * 2^-24 < 4e-6 ymax, and
+the rounding's half step is taken of a value that may be off by that much.
 """
 import ctypes
 
