@@ -185,7 +185,7 @@ __device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint
                                     uint32_t* tmem_base) {
   using C = BS<DI, N>;
   constexpr int CPR = DI / 8;  // eight-value chunks per row
-  const int64_t c = a.ctx[b];
+  const int64_t c = __ldcg(a.ctx + b);  // (loads by L2 alone: see the kernel)
   if (c < 0 || c >= a.capacity) return;
   const int64_t f = c / a.B;
   const int64_t lo = int64_t(tile) * kBlkTile;
@@ -201,8 +201,8 @@ __device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint
     const int e = tid + u * kNT;  // (row, chunk) = (e / CPR, e % CPR)
     x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (e / CPR < n) {
-      x[u][0] = __ldg(src + 2 * e);
-      x[u][1] = __ldg(src + 2 * e + 1);
+      x[u][0] = __ldcg(src + 2 * e);
+      x[u][1] = __ldcg(src + 2 * e + 1);
     }
   }
   if (warp == 0) { tmem_alloc(tmem_base, C::TMEM_COLS); tmem_relinquish(); }
@@ -210,7 +210,7 @@ __device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint
   for (int e = tid; e < a.T * CPR; e += kNT) {  // (columns past the nodes hold anything: nobody reads them)
     const int r = e / CPR, ch = e % CPR;
     *reinterpret_cast<uint4*>(sm + C::OFF_Q + (ch >> 3) * (N * 128) + swz_offset(r, ch & 7, 128)) =
-        __ldg(reinterpret_cast<const uint4*>(a.q_new + b * a.T * DI) + e);
+        __ldcg(reinterpret_cast<const uint4*>(a.q_new + b * a.T * DI) + e);
   }
 #pragma unroll
   for (int u = 0; u < PER; ++u) {
@@ -288,8 +288,10 @@ __global__ void __launch_bounds__(kNT) tree_tails_kernel(const TreeArgs a) {
 
 // Launched dependent on the tails and run beside them: its CTAs start once
 // every tail CTA has passed its own wait for the work before it, which is all
-// that the scores depend on. The wait at the end makes the kernels after this
-// one, which wait for it alone, wait for the tails too.
+// that the scores depend on. That work's writes are in L2 by then; with no wait
+// of its own this kernel reads its inputs there (an L1 might hold older lines).
+// The wait at the end makes the kernels after this one, which wait for it alone,
+// wait for the tails too.
 template <int DI, int N>
 __global__ void __launch_bounds__(kNT) tree_block_scores_kernel(const TreeArgs a) {
   extern __shared__ uint8_t smem_raw[];

@@ -275,6 +275,43 @@ def test_step_1m_context(hsa):
 
 
 @pytest.mark.gpu
+def test_caches_of_more_than_2_31_values(hsa):
+    """The last of 2064 sequences in caches of 2.16e9 values each gives what it gives alone; a step and a commit."""
+    import torch
+    big, cap, T = 2064, 8192, 3
+    c = Case(hsa, ctx=[8100], T=T, capacity=cap, B=128, m=8, k=300, d_idx=128, H=8, d=128, kind="chain", seed=3)
+    assert big * cap * c.d > 1 << 31
+    g1 = dict(c.g)
+    g = {}
+    for n in ("kc", "Kc", "Vc"):
+        g[n] = torch.empty((big, cap, 128), dtype=torch.bfloat16, device="cuda")
+        g[n][-1] = g1[n][0]
+    g["ksum"] = torch.empty((big, cap // 128, 128), device="cuda")
+    g["ksum"][-1] = g1["ksum"][0]
+    g["ctx"] = torch.full((big,), -1, dtype=torch.int32, device="cuda")
+    g["ctx"][-1] = 8100
+    for n in ("q", "kn", "Q", "Kn", "Vn"):
+        g[n] = torch.zeros((big, *g1[n].shape[1:]), dtype=torch.bfloat16, device="cuda")
+        g[n][-1] = g1[n][0]
+    g["pos"] = torch.full((big, T), -1, dtype=torch.int32, device="cuda")
+    g["pos"][-1] = g1["pos"][0]
+    g["paths"] = torch.full((big, T, T), -1, dtype=torch.int32, device="cuda")
+    g["paths"][-1] = g1["paths"][0]
+    want_O, want_idx = c.run()
+    c.g, c.batch = g, big
+    O, idx = c.run()
+    assert torch.equal(O[-1].view(torch.int16), want_O[0].view(torch.int16)) and torch.equal(idx[-1], want_idx[0])
+    assert (O[:-1] == 0).all() and (idx[:-1] == -1).all()
+    acc = torch.full((big,), -1, dtype=torch.int32, device="cuda")
+    acc[-1] = T - 1
+    for gg, b, a in ((g, big, acc), (g1, 1, acc[-1:].clone())):
+        hsa.hsa_tree_commit(c.p, b, T, cap, gg["ctx"], gg["paths"], a, gg["kc"], gg["Kc"], gg["Vc"], gg["ksum"])
+    for n in ("kc", "Kc", "Vc"):
+        assert torch.equal(g[n][-1].view(torch.int16), g1[n][0].view(torch.int16)), n
+    assert int(g["ctx"][-1]) == 8103 and (g["ctx"][:-1] == -1).all()
+
+
+@pytest.mark.gpu
 def test_one_node_is_a_decode_step(hsa):
     import torch
     kw = dict(B=64, m=8, k=256, d_idx=64, H=4, d=64)
