@@ -73,7 +73,7 @@ struct TA {
   static constexpr int SMEM = OFF_Z + Z_BYTES + 1024;  // + alignment slack
   static constexpr int TMEM_COLS = (kSB + kOB) * HP > 256 ? 512 : (kSB + kOB) * HP > 128 ? 256 : 128;
   static constexpr uint32_t P_SWZ = P_ROW == 128 ? kSw128 : P_ROW == 64 ? kSw64 : kSw32;
-  static constexpr int NWARPS = 4 + 2 + kGroups * kGroupWarps;
+  static constexpr int NWARPS = 4 + 2 + kGroups * kGroupWarps + 1;
 };
 
 struct Bars {
@@ -170,7 +170,7 @@ HSA_DEV void produce(const Args& a, uint8_t* sm, Bars& bars, int pw, int w0, int
   uint64_t* empty = IS_K ? bars.kempty : bars.vempty;
   constexpr int NS = IS_K ? C::NSK : C::NSV;
   bool dead = false;
-  uint32_t g = 0, qn = 0;
+  uint32_t g = 0;
   Item it = w0 < w1 ? read_item(a.items, w0) : Item{};
   auto rows_of = [&](const Item& x, int i, int (&j)[2]) {
     const int32_t* row = a.idx + int64_t(x.row) * a.k;
@@ -180,22 +180,10 @@ HSA_DEV void produce(const Args& a, uint8_t* sm, Bars& bars, int pw, int w0, int
   auto in_cache = [&](int j) { return j >= 0 && j < a.capacity ? j : 0; };
   int jn[2] = {0, 0};
   if (w0 < w1) rows_of(it, 0, jn);
-  for (int wi = w0; wi < w1; ++wi, ++qn) {
+  for (int wi = w0; wi < w1; ++wi) {
     const Item cur = it;
     if (wi + 1 < w1) it = read_item(a.items, wi + 1);
     const uint4* src = reinterpret_cast<const uint4*>((IS_K ? a.K : a.V) + int64_t(cur.row / a.T) * a.capacity * DH) + cpk;
-    if (IS_K && pw == 0) {  // the node's HP head rows (rows past its nh heads: zeros)
-      const int qb = qn % C::NQ;
-      wait_warp(&bars.qempty[qb], ((qn / C::NQ) & 1) ^ 1, dead);
-      const uint32_t qt = smem_u32(sm + C::OFF_Q + qb * C::Q_BYTES);
-      const uint4* qsrc = reinterpret_cast<const uint4*>(a.Q) + (int64_t(cur.row) * a.H + a.h0) * C::CPR;
-      for (int e = lane; e < HP * C::CPR; e += 32) {
-        const int h = e / C::CPR, c = e % C::CPR;
-        const bool live = h < a.nh;
-        cp_async16_zfill(qt + (c >> 3) * (HP * 128) + swz_offset(h, c & 7, 128), live ? qsrc + h * C::CPR + c : qsrc, live);
-      }
-      cp_async_arrive(&bars.qfull[qb]);
-    }
     for (int i = 0; i < cur.nt; ++i, ++g) {
       const int s = g % NS, j0 = in_cache(jn[0]), j1 = in_cache(jn[1]);  // (loaded a tile ago)
       // the next tile's rows, this item's or the next one's
@@ -214,6 +202,30 @@ HSA_DEV void produce(const Args& a, uint8_t* sm, Bars& bars, int pw, int w0, int
     }
   }
   cp_async_wait_all();  // every copy has landed before the CTA may exit
+}
+
+// The items' Q: HP head rows each (rows past the launch's nh heads: zeros). A
+// warp of its own: in front of a K warp's first rows it cost them 0.9 us.
+template <int HP, int DH>
+HSA_DEV void produce_q(const Args& a, uint8_t* sm, Bars& bars, int w0, int w1) {
+  using C = TA<HP, DH>;
+  const int lane = threadIdx.x & 31;
+  bool dead = false;
+  uint32_t qn = 0;
+  for (int wi = w0; wi < w1; ++wi, ++qn) {
+    const int row = read_item(a.items, wi).row, qb = qn % C::NQ;
+    const uint32_t qt = smem_u32(sm + C::OFF_Q + qb * C::Q_BYTES);
+    const uint4* src = reinterpret_cast<const uint4*>(a.Q) + (int64_t(row) * a.H + a.h0) * C::CPR;
+    wait_warp(&bars.qempty[qb], ((qn / C::NQ) & 1) ^ 1, dead);
+#pragma unroll 8
+    for (int e = lane; e < HP * C::CPR; e += 32) {
+      const int h = e / C::CPR, c = e % C::CPR;
+      const bool live = h < a.nh;
+      cp_async16_zfill(qt + (c >> 3) * (HP * 128) + swz_offset(h, c & 7, 128), live ? src + e : src, live);
+    }
+    cp_async_arrive(&bars.qfull[qb]);
+  }
+  cp_async_wait_all();
 }
 
 template <int HP, int DH>
@@ -333,6 +345,8 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
       wait_bar(&bars.done, 0, d2);
     }
     __syncwarp();
+  } else if (warp == C::NWARPS - 1) {
+    produce_q<HP, DH>(a, sm, bars, w0, w1);
   } else {
     // ------------------------------------------------------------ softmax
     constexpr int HPT = C::HPT, CW = HPT < 16 ? HPT : 16;  // heads per thread, columns per TMEM load

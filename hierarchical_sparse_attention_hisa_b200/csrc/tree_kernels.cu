@@ -381,7 +381,7 @@ __device__ __noinline__ void attend_head(const uint16_t* K, const uint16_t* V, c
 // rows (taken again). Grid (cut, head groups), a thread per four values; the
 // parts come U at a time, every load of a group issued before any is used.
 template <int D, int U>
-__global__ void __launch_bounds__(256, U == 4 ? 6 : 4) tree_combine_kernel(const TreeArgs a, int64_t rows,
+__global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const TreeArgs a, int64_t rows,
                                                                           const uint16_t* __restrict__ Q,
                                                                           const int32_t* __restrict__ idx, float scale,
                                                                           const float* __restrict__ Opart,
@@ -393,16 +393,8 @@ __global__ void __launch_bounds__(256, U == 4 ? 6 : 4) tree_combine_kernel(const
   griddep_launch();
   const int H = a.H, v = threadIdx.x % TPH;
   const int4 cut = a.cut[blockIdx.x];
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
-    if (a.flags[row]) {
-      const int64_t base = row / a.T * a.capacity * D;
-      const int n = min(a.k, candidates(a.rowpos[row], a.B, a.m));
-      for (int h = blockIdx.y * 8 + threadIdx.x / 32; h < H; h += gridDim.y * 8)
-        attend_head<D>(a.K_cache + base, a.V_cache + base, idx + row * a.k, n, Q + (row * H + h) * D, scale,
-                       p_s[threadIdx.x / 32], a.O + (row * H + h) * D);
-    }
-  if (cut.x < 0 || a.flags[cut.x]) return;
-  for (int h = blockIdx.y * HPC + threadIdx.x / TPH; h < H; h += gridDim.y * HPC) {
+  const int skip = cut.x < 0 ? 1 : a.flags[cut.x];  // (its load is not waited for until a store)
+  for (int h = blockIdx.y * HPC + threadIdx.x / TPH; cut.x >= 0 && h < H; h += gridDim.y * HPC) {
     float M = -INFINITY, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = 0; p0 < cut.z; p0 += U) {
@@ -432,9 +424,18 @@ __global__ void __launch_bounds__(256, U == 4 ? 6 : 4) tree_combine_kernel(const
       }
     }
     const float inv = 1.f / den;
-    reinterpret_cast<uint2*>(a.O + (int64_t(cut.x) * H + h) * D)[v] =
-        make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
+    if (!skip)
+      reinterpret_cast<uint2*>(a.O + (int64_t(cut.x) * H + h) * D)[v] =
+          make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
   }
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
+    if (a.flags[row]) {
+      const int64_t base = row / a.T * a.capacity * D;
+      const int n = min(a.k, candidates(a.rowpos[row], a.B, a.m));
+      for (int h = blockIdx.y * 8 + threadIdx.x / 32; h < H; h += gridDim.y * 8)
+        attend_head<D>(a.K_cache + base, a.V_cache + base, idx + row * a.k, n, Q + (row * H + h) * D, scale,
+                       p_s[threadIdx.x / 32], a.O + (row * H + h) * D);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -575,7 +576,7 @@ void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const i
   const dim3 grid{unsigned(kTreeAttnCtas), unsigned((a.H * a.d + 1023) / 1024)};
   count_launches(1);
   // few rows are cut into many parts, many rows into two: there fewer registers put the grid into one wave
-  auto kern = rows <= 64 ? (a.d == 128 ? tree_combine_kernel<128, 8> : tree_combine_kernel<64, 8>)
+  auto kern = rows <= 64 ? (a.d == 128 ? tree_combine_kernel<128, 16> : tree_combine_kernel<64, 16>)
                          : (a.d == 128 ? tree_combine_kernel<128, 4> : tree_combine_kernel<64, 4>);
   launch_kernel(true, kern, grid, 256, 0, s, a, rows, (const uint16_t*)Q, idx, scale, Opart, mpart, lpart);
 }
