@@ -566,8 +566,12 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   if (!hsa::launch_tree_block_scores(a, batch, p->d_idx, stream)) return HSA_ERR_CUDA;
   hsa::launch_tree_topm(a, w.rows, blocks, stream);
   // 2. token scores of the kept blocks, each cached block read once for all its nodes; top-k
-  hsa::launch_tree_lists(a, batch, stream);
-  if (!hsa::launch_tree_token_scores(a, batch, p->d_idx, w.max_items, stream)) return HSA_ERR_CUDA;
+  if (hsa::tree_few_scores(a, w.rows, p->d_idx)) {
+    hsa::launch_tree_few_scores(a, w.rows, p->d_idx, stream);
+  } else {
+    hsa::launch_tree_lists(a, batch, stream);
+    if (!hsa::launch_tree_token_scores(a, batch, p->d_idx, w.max_items, stream)) return HSA_ERR_CUDA;
+  }
   if (hsa::tree_topk_wide(a, w.rows)) {
     hsa::launch_tree_topk(a, w.rows, idx, stream);
   } else {

@@ -117,6 +117,10 @@ void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, co
                       const int32_t* parents, int32_t* positions, int32_t* paths, cudaStream_t s);
 // (also appends the drafted rows to the caches, scores every node's tail, and zeroes the O of nodes that take no part)
 bool launch_tree_block_scores(const TreeArgs& a, int batch, int d_idx, cudaStream_t s);
+// Whether the token scores are few enough to be made without lists (launch_tree_few_scores; else
+// launch_tree_lists, then launch_tree_token_scores). Both also cut the attention's work.
+bool tree_few_scores(const TreeArgs& a, int64_t rows, int d_idx);
+void launch_tree_few_scores(const TreeArgs& a, int64_t rows, int d_idx, cudaStream_t s);
 void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s);
 bool launch_tree_token_scores(const TreeArgs& a, int batch, int d_idx, int64_t max_items, cudaStream_t s);
 void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStream_t s);

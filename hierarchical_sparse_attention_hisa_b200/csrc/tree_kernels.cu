@@ -74,6 +74,7 @@ constexpr int kListNT = 512;
 // kTreeAttnCtas equal shares (what a row keeps follows from its position
 // alone). A row per CTA leaves most SMs idle when trees are ragged; with equal
 // shares at most two rows of a CTA are cut, whose parts are combined.
+template <int NT>
 __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
   const int tid = threadIdx.x;
   auto kept_of = [&](int64_t row) -> int {
@@ -82,24 +83,24 @@ __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
     return min(a.k, candidates(t, a.B, a.m));
   };
   int64_t total = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
+  for (int64_t r0 = 0; r0 < rows; r0 += NT) {
     int sum;
-    block_exclusive_scan<kListNT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
+    block_exclusive_scan<NT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
     total += sum;
   }
   const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
   int64_t tile0 = 0;
   int item0 = 0, part0 = 0, cut0 = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += kListNT) {
+  for (int64_t r0 = 0; r0 < rows; r0 += NT) {
     const int64_t row = r0 + tid;
     const int kept = kept_of(row), n = (kept + 127) / 128;
     int sum, items, parts, cuts;
-    const int64_t s = tile0 + block_exclusive_scan<kListNT>(n, s_tmp, &sum);
+    const int64_t s = tile0 + block_exclusive_scan<NT>(n, s_tmp, &sum);
     const int64_t c0 = s / quota;
     const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
-    int at = item0 + block_exclusive_scan<kListNT>(pieces, s_tmp, &items);
-    const int part = part0 + block_exclusive_scan<kListNT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
-    const int ncut = cut0 + block_exclusive_scan<kListNT>(pieces > 1, s_tmp, &cuts);
+    int at = item0 + block_exclusive_scan<NT>(pieces, s_tmp, &items);
+    const int part = part0 + block_exclusive_scan<NT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
+    const int ncut = cut0 + block_exclusive_scan<NT>(pieces > 1, s_tmp, &cuts);
     if (row < rows) a.flags[row] = 0;
     if (pieces > 1) a.cut[ncut] = make_int4(int(row), part, pieces, 0);
     for (int j = 0; j < pieces; ++j, ++at) {
@@ -112,9 +113,9 @@ __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
     part0 += parts;
     cut0 += cuts;
   }
-  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += kListNT) a.cta_items[c] = item0;
+  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += NT) a.cta_items[c] = item0;
   // (a cut lies between two CTAs, so fewer rows than CTAs are cut)
-  for (int c = cut0 + tid; c < kTreeAttnCtas; c += kListNT) a.cut[c] = make_int4(-1, 0, 0, 0);
+  for (int c = cut0 + tid; c < kTreeAttnCtas; c += NT) a.cut[c] = make_int4(-1, 0, 0, 0);
 }
 
 __device__ void tail_keys(const TreeArgs& a, int64_t row) {  // a warp per node
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, i
   griddep_wait();
   griddep_launch();
   if (blockIdx.x == gridDim.x - 1) {
-    attn_shares(a, int64_t(batch) * a.T, s_tmp);
+    attn_shares<kListNT>(a, int64_t(batch) * a.T, s_tmp);
     return;
   }
   if (int(blockIdx.x) >= batch * ranges) {
@@ -206,6 +207,64 @@ __global__ void __launch_bounds__(kListNT) tree_lists_kernel(const TreeArgs a, i
     const int i = e / a.m;
     pairs[atomicAdd(&hist[blk - lo], 1)] = uint32_t(i) << 16 | uint32_t(e - i * a.m);
   });
+}
+
+// ---------------------------------------------------------------------------
+// Token scores of few nodes without lists: grid (node, slot), a CTA per kept
+// block of each node, on CUDA cores. A block that several nodes kept is read by
+// each (from L2), but no list has to be made first: that launch costs more than
+// the reading as long as there is little of it (see tree_few_scores).
+// ---------------------------------------------------------------------------
+constexpr int kFewNT = 128;
+
+template <int DI>
+__global__ void __launch_bounds__(kFewNT) tree_few_scores_kernel(const TreeArgs a, int64_t rows) {
+  __shared__ int s_tmp[kFewNT / 32 + 1];
+  griddep_wait();
+  griddep_launch();
+  if (int(blockIdx.y) == a.m) {
+    if (blockIdx.x == 0) attn_shares<kFewNT>(a, rows, s_tmp);
+    return;
+  }
+  const int64_t row = blockIdx.x, b = row / a.T;
+  const int blk = a.blocks[row * a.m + blockIdx.y];
+  const int t = a.rowpos[row], c = a.ctx[b];
+  constexpr int LPR = DI / 8, RPC = kFewNT / LPR, U = 8;  // lanes per key row, rows per CTA at a time, turns in flight
+  const int sub = threadIdx.x % LPR, r1 = threadIdx.x / LPR;
+  const uint4 qv = __ldg(reinterpret_cast<const uint4*>(a.q_new + row * DI) + sub);
+  if (t < 0 || blk < 0 || candidates(t, a.B, a.m) <= a.k) return;
+  uint32_t* out = a.tkeys + (row * a.m + blockIdx.y) * int64_t(a.B);
+  const int f = c / a.B;
+  if (blk >= f) {  // a tail block
+    const uint32_t* src = a.tailkeys + row * a.tail_ld + (blk - f) * a.B;
+    const int n = min(a.B, t - blk * a.B + 1);
+    for (int r = threadIdx.x; r < n; r += kFewNT) out[r] = src[r];
+    return;
+  }
+  const uint4* kb = reinterpret_cast<const uint4*>(a.k_idx_cache + (b * a.capacity + int64_t(blk) * a.B) * DI) + sub;
+  const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w};
+  for (int r0 = r1; r0 < a.B + r1; r0 += RPC * U) {  // (every lane of a warp takes part in the sums)
+    uint4 kv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * RPC;
+      kv[u] = r < a.B ? __ldg(kb + int64_t(r) * LPR) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t kw[4] = {kv[u].x, kv[u].y, kv[u].z, kv[u].w};
+      float acc = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc = __fmaf_rn(bf16_lo(qw[e]), bf16_lo(kw[e]), acc);
+        acc = __fmaf_rn(bf16_hi(qw[e]), bf16_hi(kw[e]), acc);
+      }
+#pragma unroll
+      for (int o = LPR / 2; o >= 1; o >>= 1) acc += __shfl_xor_sync(kFull, acc, o);
+      const int r = r0 + u * RPC;
+      if (sub == 0 && r < a.B) out[r] = score_key(acc);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -541,6 +600,20 @@ void launch_tree_lists(const TreeArgs& a, int batch, cudaStream_t s) {
   launch_kernel(true, tree_lists_kernel, unsigned(batch * ranges) + tails + 1, kListNT, 0, s, a, batch, ranges);
 }
 
+bool tree_few_scores(const TreeArgs& a, int64_t rows, int d_idx) {
+  // by the bytes that all nodes' kept blocks have. A whole step with lists / without them: 42.2 / 37.2 us at
+  // 16 MB (8 nodes, m = 64, B = 128), 51.4 / 49.2 at 64 MB (32 nodes), 55.0 / 53.8 at 128 MB (8 x 8 nodes),
+  // 62.5 / 65.3 at 256 MB (16 x 8 nodes)
+  return rows * a.m * a.B * int64_t(d_idx) * 2 <= int64_t(128) << 20;
+}
+
+void launch_tree_few_scores(const TreeArgs& a, int64_t rows, int d_idx, cudaStream_t s) {
+  const dim3 grid{unsigned(rows), unsigned(a.m + 1)};
+  count_launches(1);
+  launch_kernel(true, d_idx == 128 ? tree_few_scores_kernel<128> : tree_few_scores_kernel<64>, grid, kFewNT, 0, s, a,
+                rows);
+}
+
 void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStream_t s) {
   const int64_t n = a.capacity / a.B;
   count_launches(1);
@@ -576,7 +649,7 @@ void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const i
   const dim3 grid{unsigned(kTreeAttnCtas), unsigned((a.H * a.d + 1023) / 1024)};
   count_launches(1);
   // few rows are cut into many parts, many rows into two: there fewer registers put the grid into one wave
-  auto kern = rows <= 64 ? (a.d == 128 ? tree_combine_kernel<128, 16> : tree_combine_kernel<64, 16>)
+  auto kern = rows <= 32 ? (a.d == 128 ? tree_combine_kernel<128, 16> : tree_combine_kernel<64, 16>)
                          : (a.d == 128 ? tree_combine_kernel<128, 4> : tree_combine_kernel<64, 4>);
   launch_kernel(true, kern, grid, 256, 0, s, a, rows, (const uint16_t*)Q, idx, scale, Opart, mpart, lpart);
 }

@@ -208,6 +208,16 @@ STEP_CASES = {
     # 640 and 1280 rows: the selections for many rows
     "rows_640": dict(SMALL, ctx=list(range(955, 855, -10)), T=64, capacity=1024, kind="random"),
     "rows_1280": dict(B=100, m=5, k=130, d_idx=128, H=2, d=64, ctx=list(range(1950, 1930, -1)), T=64, capacity=2100),
+    # more than 128 MB of kept blocks: the token scores go through work lists. One row, odd, whole, two and eight
+    # pieces of 128 rows per block; small blocks that a path completes
+    "lists_1": dict(B=1, m=512, k=300, d_idx=128, H=2, d=64, ctx=list(range(700, 717)), T=64, capacity=800),
+    "lists_7": dict(B=7, m=512, k=900, d_idx=128, H=4, d=128, ctx=[4200, 3900, 4201], T=64, capacity=4270),
+    "lists_16": dict(B=16, m=400, k=1500, d_idx=128, H=2, d=64, ctx=[7000, 6900], T=50, capacity=7104, kind="chain"),
+    "lists_100": dict(B=100, m=80, k=700, d_idx=128, H=16, d=64, ctx=[9950, 9001], T=40, capacity=10100, kind="binary"),
+    "lists_64": dict(B=64, m=200, k=2000, d_idx=64, H=4, d=128, ctx=[16000, 15000], T=48, capacity=16384),
+    "lists_200": dict(B=200, m=70, k=500, d_idx=128, H=8, d=128, ctx=[17990, 15001], T=32, capacity=18200),
+    "lists_256": dict(B=256, m=64, k=2048, d_idx=128, H=64, d=128, ctx=[18000, 17919], T=20, capacity=18176),
+    "lists_1024": dict(B=1024, m=16, k=500, d_idx=128, H=1, d=64, ctx=[18420, 17000], T=20, capacity=19456, kind="chain"),
     "wide_rows": dict(B=64, m=300, k=1000, d_idx=64, H=4, d=64, ctx=[30000, 20095], T=6, capacity=32768),
     "scaled": dict(SMALL, ctx=[900], T=6, capacity=1024, scale=0.7),
     # logits hundreds of nats apart: weights that leave the range of a list's first tile
@@ -226,7 +236,8 @@ def test_step_against_oracle(hsa, name):
     c = Case(hsa, **STEP_CASES[name])
     O, idx = c.run()
     rows = c.batch * c.T
-    c.check(O, idx, None if rows <= 400 else {(b, i) for b in range(c.batch) for i in range(b % 7, c.T, 11)})
+    some = {(b, i) for b in range(c.batch) for i in range(b % 7, c.T, 11)}
+    c.check(O, idx, some if rows > 400 or name.startswith("lists") else None)
     c.check_caches()
     # the same call again, over rows drafted before: the same bits
     O2, idx2 = c.run()
@@ -236,7 +247,7 @@ def test_step_against_oracle(hsa, name):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("name", ["ragged", "block_200", "rows_200", "many_heads"])
+@pytest.mark.parametrize("name", ["ragged", "block_200", "rows_200", "many_heads", "lists_200"])
 def test_rows_that_are_not_kept_do_not_matter(hsa, name):
     """NaN and infinities behind the drafted rows, and in the K and V rows that no node keeps."""
     import torch
@@ -355,7 +366,7 @@ def test_stale_plan_reaches_nothing_outside(hsa):
 def test_step_stays_inside_its_buffers(hsa):
     import torch
     guard, fill = 4096, 0xA5
-    for name in ("ragged", "block_200", "odd_k", "rows_200"):
+    for name in ("ragged", "block_200", "odd_k", "rows_200", "lists_7", "lists_200"):
         c = Case(hsa, **STEP_CASES[name])
         want_O, want_idx = c.run()
         sizes = dict(ws=hsa.hsa_tree_workspace_size(c.p, c.batch, c.T, c.capacity), O=want_O.numel() * 2,
@@ -390,7 +401,7 @@ def test_step_without_indices_and_on_another_stream(hsa):
 def test_two_steps_at_once(hsa):
     """Two calls on two streams, each with its own caches and workspace."""
     import torch
-    cases = [Case(hsa, **dict(STEP_CASES[n], seed=s)) for n, s in (("rows_200", 5), ("block_256", 6))]
+    cases = [Case(hsa, **dict(STEP_CASES[n], seed=s)) for n, s in (("lists_256", 5), ("block_256", 6))]
     want = [c.run() for c in cases]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in cases]

@@ -13,7 +13,7 @@ def test_lost_item_times_out_and_recovers():
     from hierarchical_sparse_attention_hisa_b200._lib import HSA_ERR_TIMEOUT, HSA_OK
     from test_tree import STEP_CASES, Case
     hsa.build()
-    c = Case(hsa, **STEP_CASES["rows_200"])
+    c = Case(hsa, **STEP_CASES["lists_100"])
     O, idx = c.run()
     torch.cuda.synchronize()
     assert hsa.hsa_device_status(reset=True) == HSA_OK
