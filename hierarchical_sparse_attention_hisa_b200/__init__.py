@@ -82,6 +82,8 @@ def qk_norm_rope(Q, K, q_weight=None, k_weight=None, inv_freq=None, positions=No
         if t is not None and (t.dtype != dtype or t.device != ref.device or not t.is_contiguous() or t.dim() != 1
                               or (shape and tuple(t.shape) != shape)):
             raise ValueError(f"{name}: expected a contiguous 1-d {dtype} tensor on the same device")
+    if ref.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current device")
     H = Q.shape[1] if Q is not None else 1
     rot = 2 * inv_freq.numel() if inv_freq is not None else 0
     new = torch.empty if positions is None else torch.zeros

@@ -106,7 +106,10 @@ def status_string(status: int) -> str:
 
 
 def params(B=128, m=64, k=2048, d_idx=128, H=64, d=128, scale=0.0) -> hsa_params:
-    return hsa_params(int(B), int(m), int(k), int(d_idx), int(H), int(d), float(scale))
+    try:
+        return hsa_params(B, m, k, d_idx, H, d, scale)
+    except TypeError:  # integers of other kinds (numpy's)
+        return hsa_params(int(B), int(m), int(k), int(d_idx), int(H), int(d), float(scale))
 
 
 def _p(t):
@@ -114,10 +117,19 @@ def _p(t):
     return None if t is None else t.data_ptr() or None
 
 
+def _current():
+    """Handle of the current device's current stream (rebound on first use: a Stream object costs 1 us a call)."""
+    global _current
+    import torch
+    torch.cuda.init()
+    stream, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _current = lambda: stream(device())  # noqa: E731
+    return _current()
+
+
 def _s(stream):
-    if stream is None:  # the current device's current stream, without building a Stream object (about 1 us a call)
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return _current()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -208,21 +220,28 @@ def hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, inte
     """Row strides are the tensors' own; a token's heads and values must be contiguous."""
     q_stride = k_stride = 0
     if Q is not None:
-        if Q.stride(-1) != 1 or Q.stride(-2) != d:
+        st = Q.stride()
+        if st[-1] != 1 or (H > 1 and st[-2] != d):
             raise ValueError("Q: the heads of a token must be contiguous")
-        q_stride = Q.stride(0) if L > 1 else H * d
+        q_stride = st[0] if L > 1 else H * d
     if K is not None:
-        if K.stride(-1) != 1:
+        st = K.stride()
+        if st[-1] != 1:
             raise ValueError("K: the values of a row must be contiguous")
-        k_stride = K.stride(0) if L > 1 else d
-    _check("hsa_qk_norm_rope", load().hsa_qk_norm_rope(
+        k_stride = st[0] if L > 1 else d
+    st = (_lib or load()).hsa_qk_norm_rope(
         L, H, d, _p(Q), q_stride, _p(K), k_stride, _p(q_weight), _p(k_weight), eps, _p(inv_freq), rot,
-        1 if interleaved else 0, _p(positions), pos0, _p(Q_out), _p(K_out), _s(stream)))
+        1 if interleaved else 0, _p(positions), pos0, _p(Q_out), _p(K_out), _s(stream))
+    if st:
+        raise HSAError("hsa_qk_norm_rope", st)
 
 
 def hsa_tree_plan(batch, T, capacity, ctx_len, n_nodes, parents, positions, paths, stream=None):
-    _check("hsa_tree_plan", load().hsa_tree_plan(
-        batch, T, capacity, _p(ctx_len), _p(n_nodes), _p(parents), _p(positions), _p(paths), _s(stream)))
+    st = (_lib or load()).hsa_tree_plan(
+        batch, T, capacity, ctx_len.data_ptr(), _p(n_nodes), parents.data_ptr(), positions.data_ptr(),
+        paths.data_ptr(), _s(stream))
+    if st:
+        raise HSAError("hsa_tree_plan", st)
 
 
 def hsa_tree_workspace_size(p, batch, T, capacity) -> int:
@@ -234,15 +253,20 @@ def hsa_tree_workspace_size(p, batch, T, capacity) -> int:
 
 def hsa_tree_step(p, batch, T, capacity, ctx_len, positions, paths, k_idx_cache, K_cache, V_cache, ksum_cache,
                   q_idx_new, k_idx_new, Q_new, K_new, V_new, O, indices_out, workspace, stream=None):
-    _check("hsa_tree_step", load().hsa_tree_step(
-        ctypes.byref(p), batch, T, capacity, _p(ctx_len), _p(positions), _p(paths), _p(k_idx_cache),
-        _p(K_cache), _p(V_cache), _p(ksum_cache), _p(q_idx_new), _p(k_idx_new), _p(Q_new), _p(K_new),
-        _p(V_new), _p(O), _p(indices_out), _p(workspace), workspace.numel() * workspace.element_size(),
-        _s(stream)))
+    st = (_lib or load()).hsa_tree_step(
+        ctypes.byref(p), batch, T, capacity, ctx_len.data_ptr(), positions.data_ptr(), paths.data_ptr(),
+        k_idx_cache.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), ksum_cache.data_ptr(),
+        q_idx_new.data_ptr(), k_idx_new.data_ptr(), Q_new.data_ptr(), K_new.data_ptr(), V_new.data_ptr(),
+        O.data_ptr(), _p(indices_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _s(stream))
+    if st:
+        raise HSAError("hsa_tree_step", st)
 
 
 def hsa_tree_commit(p, batch, T, capacity, ctx_len, paths, accepted, k_idx_cache, K_cache, V_cache, ksum_cache,
                     stream=None):
-    _check("hsa_tree_commit", load().hsa_tree_commit(
-        ctypes.byref(p), batch, T, capacity, _p(ctx_len), _p(paths), _p(accepted), _p(k_idx_cache),
-        _p(K_cache), _p(V_cache), _p(ksum_cache), _s(stream)))
+    st = (_lib or load()).hsa_tree_commit(
+        ctypes.byref(p), batch, T, capacity, ctx_len.data_ptr(), paths.data_ptr(), accepted.data_ptr(),
+        k_idx_cache.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), ksum_cache.data_ptr(), _s(stream))
+    if st:
+        raise HSAError("hsa_tree_commit", st)

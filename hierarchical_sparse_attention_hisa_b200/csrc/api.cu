@@ -442,13 +442,13 @@ extern "C" int hsa_qk_norm_rope(int64_t L, int32_t H, int32_t d, const hsa_bf16*
 namespace {
 
 // Workspace of a tree step (256-byte aligned regions), rows = batch * T:
-//   counters [2] i32, rowpos [rows] i32, block-score keys [rows][ldb] u32, tail
+//   counters [3] i32, rowpos [rows] i32, block-score keys [rows][ldb] u32, tail
 //   keys [rows][tail_ld] u32, kept blocks [rows][m] i32, pairs [rows][m] u32,
 //   items [max_items] int4, token-score keys [rows][m*B] u32, indices [rows][k]
 //   i32 (unless the caller takes them), the attention's items, their CTAs' first
 //   ones, the rows that are cut, the rows' flags, and the parts: O f32, maxima and row sums f32.
 struct TreeWs {
-  size_t counters, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, aitems, cta, cut, flags, opart, mpart, lpart,
+  size_t counters, rowpos, bkeys, tail, blocks, pairs, items, tkeys, idx, aitems, cta, cut, flags, flagged, opart, mpart, lpart,
       total;
   int64_t rows, ldb, max_items;
   int tail_ld;
@@ -463,7 +463,7 @@ TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) 
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += align_up(bytes > 0 ? bytes : 1); return at; };
   const size_t rows = size_t(w.rows);
-  w.counters = take(8);
+  w.counters = take(12);
   w.rowpos = take(rows * 4);
   w.bkeys = take(rows * w.ldb * 4);
   w.tail = take(rows * w.tail_ld * 4);
@@ -478,6 +478,7 @@ TreeWs tree_ws(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity) 
   w.cta = take((hsa::kTreeAttnCtas + 1) * 4);
   w.cut = take(hsa::kTreeAttnCtas * 16);
   w.flags = take(rows * 4);
+  w.flagged = take(rows * 4);
   w.opart = take(parts * p->H * p->d * 4);
   w.mpart = take(parts * p->H * 4);
   w.lpart = take(parts * p->H * 4);
@@ -492,7 +493,7 @@ int check_tree_sizes(const hsa_params* p, int32_t batch, int32_t T, int64_t capa
   // cache rows and (node, slot) pairs are counted in 32 bits, sequences in 28
   if (batch > 0 && (capacity > kMax / batch || int64_t(batch) * T > kMax / p->m || batch >= (1 << 28)))
     return HSA_ERR_ARG;
-  if (int64_t(batch) * T > kMax / p->H) return HSA_ERR_ARG;
+  if (int64_t(batch) * T > kMax / std::max(p->H, 64)) return HSA_ERR_ARG;  // (also: at most 64 tiles per node)
   return HSA_OK;
 }
 
@@ -561,6 +562,7 @@ int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacit
   a.cut = reinterpret_cast<int4*>(ws + w.cut);
   a.O = O; a.H = p->H;
   a.flags = reinterpret_cast<int*>(ws + w.flags);
+  a.flagged = reinterpret_cast<int*>(ws + w.flagged);
   // The kernels are programmatic dependent launches, as in a decode step.
   // 1. drafted rows appended, tails and cached blocks scored; top-m
   if (!hsa::launch_tree_block_scores(a, batch, p->d_idx, stream)) return HSA_ERR_CUDA;

@@ -93,7 +93,7 @@ struct Args {
   const int* cta_items;
   uint16_t* O;
   float *Opart, *mpart, *lpart;
-  int* flags;
+  int *flags, *flagged, *n_flagged;
 };
 
 // Bounded wait. A failed probe goes straight back to the barrier: the limit,
@@ -466,7 +466,8 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
         }
         linv[sg][r] = l > 0.f ? 1.f / l : 0.f;
         if (r < a.nh && !dead) {
-          if (!(l > 0.f && l <= 1152921504606846976.f)) a.flags[cur.row] = 1;  // 2^60
+          if (!(l > 0.f && l <= 1152921504606846976.f) && atomicExch(a.flags + cur.row, 1) == 0)  // 2^60
+            a.flagged[atomicAdd(a.n_flagged, 1)] = cur.row;
           if (cur.part >= 0) {
             a.mpart[int64_t(cur.part) * a.H + a.h0 + r] = -neg_m[ib][r];
             a.lpart[int64_t(cur.part) * a.H + a.h0 + r] = l;
@@ -538,7 +539,7 @@ bool launch_tree_attn(const TreeArgs& t, const void* Q, const int32_t* idx, floa
   a.items = t.attn_items; a.cta_items = t.cta_items;
   a.O = t.O;
   a.Opart = Opart; a.mpart = mpart; a.lpart = lpart;
-  a.flags = t.flags;
+  a.flags = t.flags; a.flagged = t.flagged; a.n_flagged = t.counters + 2;
   for (int h0 = 0; h0 < t.H; h0 += 64) {
     a.h0 = h0;
     a.nh = t.H - h0 < 64 ? t.H - h0 : 64;

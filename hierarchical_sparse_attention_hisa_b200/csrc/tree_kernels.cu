@@ -77,45 +77,50 @@ constexpr int kListNT = 512;
 template <int NT>
 __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
   const int tid = threadIdx.x;
+  const int64_t per = (rows + NT - 1) / NT;  // a thread has `per` rows in a row, and looks at them three times
+  const int64_t r0 = min(rows, tid * per), r1 = min(rows, r0 + per);
   auto kept_of = [&](int64_t row) -> int {
-    const int t = row < rows ? a.rowpos[row] : -1;
-    if (t < 0) return 0;
-    return min(a.k, candidates(t, a.B, a.m));
+    const int t = a.rowpos[row];
+    return t < 0 ? 0 : min(a.k, candidates(t, a.B, a.m));
   };
-  int64_t total = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += NT) {
-    int sum;
-    block_exclusive_scan<NT>((kept_of(r0 + tid) + 127) / 128, s_tmp, &sum);
-    total += sum;
-  }
-  const int64_t quota = max(int64_t(1), (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
-  int64_t tile0 = 0;
-  int item0 = 0, part0 = 0, cut0 = 0;
-  for (int64_t r0 = 0; r0 < rows; r0 += NT) {
-    const int64_t row = r0 + tid;
-    const int kept = kept_of(row), n = (kept + 127) / 128;
-    int sum, items, parts, cuts;
-    const int64_t s = tile0 + block_exclusive_scan<NT>(n, s_tmp, &sum);
-    const int64_t c0 = s / quota;
-    const int pieces = n ? int((s + n - 1) / quota - c0) + 1 : 0;
-    int at = item0 + block_exclusive_scan<NT>(pieces, s_tmp, &items);
-    const int part = part0 + block_exclusive_scan<NT>(pieces > 1 ? pieces : 0, s_tmp, &parts);
-    const int ncut = cut0 + block_exclusive_scan<NT>(pieces > 1, s_tmp, &cuts);
-    if (row < rows) a.flags[row] = 0;
-    if (pieces > 1) a.cut[ncut] = make_int4(int(row), part, pieces, 0);
+  int mine = 0, total;  // (at most 64 tiles per row, 2^31 / m rows)
+#pragma unroll 4
+  for (int64_t row = r0; row < r1; ++row) mine += (kept_of(row) + 127) / 128;
+  const int tile0 = block_exclusive_scan<NT>(mine, s_tmp, &total);
+  const int quota = max(1, (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
+  // f(row, kept rows, first tile, tiles, pieces): a row's tiles lie in `pieces` CTAs
+  auto for_rows = [&](auto fn) {
+    int s = tile0;
+#pragma unroll 4
+    for (int64_t row = r0; row < r1; ++row) {
+      const int kept = kept_of(row), n = (kept + 127) / 128;
+      fn(row, kept, s, n, n ? (s + n - 1) / quota - s / quota + 1 : 0);
+      s += n;
+    }
+  };
+  int items = 0, parts = 0, cuts = 0;
+  for_rows([&](int64_t row, int, int, int, int pieces) {
+    a.flags[row] = 0;
+    items += pieces;
+    parts += pieces > 1 ? pieces : 0;
+    cuts += pieces > 1;
+  });
+  int all_items, all_parts, all_cuts;
+  int at = block_exclusive_scan<NT>(items, s_tmp, &all_items);
+  int part = block_exclusive_scan<NT>(parts, s_tmp, &all_parts);
+  int cut = block_exclusive_scan<NT>(cuts, s_tmp, &all_cuts);
+  for_rows([&](int64_t row, int kept, int s, int n, int pieces) {
+    if (pieces > 1) a.cut[cut++] = make_int4(int(row), part, pieces, 0);
+    const int c0 = s / quota;
     for (int j = 0; j < pieces; ++j, ++at) {
-      const int64_t lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
-      a.attn_items[at] = make_int4(int(row), int(lo - s) | int(hi - lo) << 8 | kept << 16, pieces > 1 ? part + j : -1, 0);
+      const int lo = max(s, (c0 + j) * quota), hi = min(s + n, (c0 + j + 1) * quota);
+      a.attn_items[at] = make_int4(int(row), (lo - s) | (hi - lo) << 8 | kept << 16, pieces > 1 ? part++ : -1, 0);
       if (lo == (c0 + j) * quota) a.cta_items[c0 + j] = at;  // the first item of CTA c0 + j
     }
-    tile0 += sum;
-    item0 += items;
-    part0 += parts;
-    cut0 += cuts;
-  }
-  for (int64_t c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += NT) a.cta_items[c] = item0;
+  });
+  for (int c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += NT) a.cta_items[c] = all_items;
   // (a cut lies between two CTAs, so fewer rows than CTAs are cut)
-  for (int c = cut0 + tid; c < kTreeAttnCtas; c += NT) a.cut[c] = make_int4(-1, 0, 0, 0);
+  for (int c = all_cuts + tid; c < kTreeAttnCtas; c += NT) a.cut[c] = make_int4(-1, 0, 0, 0);
 }
 
 __device__ void tail_keys(const TreeArgs& a, int64_t row) {  // a warp per node
@@ -440,7 +445,7 @@ __device__ __noinline__ void attend_head(const uint16_t* K, const uint16_t* V, c
 // rows (taken again). Grid (cut, head groups), a thread per four values; the
 // parts come U at a time, every load of a group issued before any is used.
 template <int D, int U>
-__global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const TreeArgs a, int64_t rows,
+__global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const TreeArgs a,
                                                                           const uint16_t* __restrict__ Q,
                                                                           const int32_t* __restrict__ idx, float scale,
                                                                           const float* __restrict__ Opart,
@@ -487,14 +492,15 @@ __global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const
       reinterpret_cast<uint2*>(a.O + (int64_t(cut.x) * H + h) * D)[v] =
           make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
   }
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x)
-    if (a.flags[row]) {
-      const int64_t base = row / a.T * a.capacity * D;
-      const int n = min(a.k, candidates(a.rowpos[row], a.B, a.m));
-      for (int h = blockIdx.y * 8 + threadIdx.x / 32; h < H; h += gridDim.y * 8)
-        attend_head<D>(a.K_cache + base, a.V_cache + base, idx + row * a.k, n, Q + (row * H + h) * D, scale,
-                       p_s[threadIdx.x / 32], a.O + (row * H + h) * D);
-    }
+  const int again = a.counters[2];
+  for (int i = blockIdx.x; i < again; i += gridDim.x) {
+    const int64_t row = a.flagged[i];
+    const int64_t base = row / a.T * a.capacity * D;
+    const int n = min(a.k, candidates(a.rowpos[row], a.B, a.m));
+    for (int h = blockIdx.y * 8 + threadIdx.x / 32; h < H; h += gridDim.y * 8)
+      attend_head<D>(a.K_cache + base, a.V_cache + base, idx + row * a.k, n, Q + (row * H + h) * D, scale,
+                     p_s[threadIdx.x / 32], a.O + (row * H + h) * D);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -651,7 +657,7 @@ void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const i
   // few rows are cut into many parts, many rows into two: there fewer registers put the grid into one wave
   auto kern = rows <= 32 ? (a.d == 128 ? tree_combine_kernel<128, 16> : tree_combine_kernel<64, 16>)
                          : (a.d == 128 ? tree_combine_kernel<128, 4> : tree_combine_kernel<64, 4>);
-  launch_kernel(true, kern, grid, 256, 0, s, a, rows, (const uint16_t*)Q, idx, scale, Opart, mpart, lpart);
+  launch_kernel(true, kern, grid, 256, 0, s, a, (const uint16_t*)Q, idx, scale, Opart, mpart, lpart);
 }
 
 void launch_tree_commit(int batch, int T, int64_t capacity, int B, int d_idx, int d, int32_t* ctx,

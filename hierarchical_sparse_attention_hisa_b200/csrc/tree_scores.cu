@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kNT) tree_tails_kernel(const TreeArgs a) {
   griddep_wait();
   griddep_launch();
   const int64_t b = blockIdx.x;
-  if (b == 0 && blockIdx.y == 0 && threadIdx.x < 2) a.counters[threadIdx.x] = 0;
+  if (b == 0 && blockIdx.y == 0 && threadIdx.x < 3) a.counters[threadIdx.x] = 0;
   const int half = threadIdx.x / kNodeNT, i = int(blockIdx.y) * kNodesPerCta + half;
   if (i < a.T) node_tail<DI>(a, b, i, threadIdx.x % kNodeNT, 1 + half, tail_smem + half * a.tail_ld);
 }

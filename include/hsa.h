@@ -316,8 +316,8 @@ HSA_API int hsa_tree_workspace_size(const hsa_params* p, int32_t batch, int32_t 
  * of each node, ascending, -1 padded (an entry below ctx_len is that position,
  * entry ctx_len + j is drafted node j). A node that takes no part writes
  * nothing to the caches; its O row is zero and its indices are -1.
- * batch * capacity, batch * T * m and batch * T * H must stay below 2^31, and
- * capacity / B is at most 16384 blocks. Calls that may overlap on the GPU
+ * batch * capacity, batch * T * m, batch * T * H and batch * T * 64 must stay
+ * below 2^31, and capacity / B is at most 16384 blocks. Calls that may overlap on the GPU
  * (other streams, several captured graphs) need workspaces of their own. */
 HSA_API int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity,
                           const int32_t* ctx_len, const int32_t* positions, const int32_t* paths,

@@ -208,6 +208,8 @@ STEP_CASES = {
     # 640 and 1280 rows: the selections for many rows
     "rows_640": dict(SMALL, ctx=list(range(955, 855, -10)), T=64, capacity=1024, kind="random"),
     "rows_1280": dict(B=100, m=5, k=130, d_idx=128, H=2, d=64, ctx=list(range(1950, 1930, -1)), T=64, capacity=2100),
+    # many rows whose keys do not all start on 16 bytes
+    "rows_odd": dict(B=7, m=3, k=11, d_idx=64, H=2, d=128, ctx=list(range(60, 70)), T=64, capacity=203),
     # more than 128 MB of kept blocks: the token scores go through work lists. One row, odd, whole, two and eight
     # pieces of 128 rows per block; small blocks that a path completes
     "lists_1": dict(B=1, m=512, k=300, d_idx=128, H=2, d=64, ctx=list(range(700, 717)), T=64, capacity=800),
