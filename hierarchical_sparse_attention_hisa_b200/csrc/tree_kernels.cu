@@ -274,8 +274,9 @@ __global__ void __launch_bounds__(kFewNT) tree_few_scores_kernel(const TreeArgs 
 
 // ---------------------------------------------------------------------------
 // Selections with a wide CTA per row, keys in registers (RegSelect): what a
-// step's latency needs, where the prefill's kernels are made for many rows.
-// At most kWideRows rows are one wave of the device.
+// step's latency needs, where the prefill's kernels are made for many rows (a
+// step of 8 nodes at 128K: 37.0 us, with 512 threads per top-k row 39.7, with
+// 256 49.0).
 //
 // Top-m: candidate c is block c + 1 of 1 .. nb-2; bkeys rows start three keys
 // in, so that block 1's key is on 16 bytes.
@@ -309,7 +310,8 @@ __global__ void __launch_bounds__(NT) tree_topm_kernel(const TreeArgs a, int32_t
 // Top-k of a node's candidates (the tokens of its kept blocks, ascending), and
 // their positions as rows of the sequence's cache.
 template <int NT, int KPT>
-__global__ void __launch_bounds__(NT, NT == 1024 && KPT <= 8 ? 2 : 1) tree_topk_kernel(const TreeArgs a, int32_t* __restrict__ idx) {
+__global__ void __launch_bounds__(NT, NT == 1024 && KPT <= 8 ? 2 : 1) tree_topk_kernel(const TreeArgs a,
+                                                                                      int32_t* __restrict__ idx) {
   __shared__ uint32_t hist[RegSelect<NT, KPT>::kBins];
   __shared__ int scratch[NT / 32 + 8];
   __shared__ int blk[512];

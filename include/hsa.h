@@ -279,7 +279,8 @@ HSA_API int hsa_qk_norm_rope(int64_t L, int32_t H, int32_t d, const hsa_bf16* Q,
  * sequence's tree is a drafted token whose parent is an earlier node, or the
  * sequence's last cached token; its path is its ancestors and itself. One
  * round: hsa_tree_plan once, hsa_tree_step in every layer, and once the caller
- * has chosen which path it accepts, hsa_tree_commit in every layer.
+ * has chosen which path it accepts, hsa_tree_commit in every layer (each layer
+ * with caches and a ctx_len array of its own, as for hsa_decode_step).
  * --------------------------------------------------------------------------- */
 #define HSA_TREE_MAX 64 /* drafted nodes per sequence */
 

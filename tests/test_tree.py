@@ -186,6 +186,7 @@ STEP_CASES = {
     # ragged lengths from none to the last row, a sequence without room, one without nodes
     "ragged": dict(SMALL, ctx=[1, 63, 500, 1000, 0, 1017, 1018, 640], T=7, capacity=1024,
                    n_nodes=[7, 7, 6, 7, 7, 7, 7, 0]),
+    "one_block": dict(B=64, m=2, k=20, d_idx=64, H=4, d=64, ctx=[0, 5, 61, 62, 64], T=3, capacity=64),
     "one_node": dict(SMALL, ctx=[5, 600, 1023], T=1, capacity=1024),
     # 64 drafted tokens in a row complete several small blocks, which then compete as candidates
     "chain_small_blocks": dict(B=16, m=6, k=40, d_idx=128, H=5, d=128, ctx=[200, 7, 0, 447], T=64, capacity=512,
