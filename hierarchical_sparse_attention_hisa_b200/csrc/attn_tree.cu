@@ -25,10 +25,11 @@
 //
 // Softmax: the maximum of an item's first tile is the reference of all its
 // tiles, no later tile looks for another. That is exact to rounding as long as
-// nothing leaves the range of fp32 and bf16 exponents: weights may grow to 2^60
-// times the first tile's largest. A row whose sum passes 2^60, is not positive
-// or not a number is flagged and taken again by tree_combine_kernel with a
-// running maximum. P is rounded to bf16 for the second MMA (2^-9 of each weight,
+// nothing leaves the range of fp32 and bf16 exponents: weights may grow to 2^90
+// times the first tile's largest (62 nats above its maximum; 2^90 times values
+// below 2^37 still fits O). Where a head's sum passes 2^90, is not positive or not
+// a number, its group of eight heads is flagged, and taken again by
+// tree_combine_kernel with a running maximum, at some 40 times the cost. P is rounded to bf16 for the second MMA (2^-9 of each weight,
 // independent from key to key), everything else is fp32, O rounded once.
 //
 // Every mbarrier wait is bounded. A thread whose wait runs out goes on through
@@ -49,6 +50,7 @@ using namespace tc;
 constexpr int TILE = 128;
 constexpr long long kInjectWaitCycles = 1ll << 21;  // about a millisecond
 constexpr int kSB = 4, kOB = 2;                     // S and O buffers in TMEM
+constexpr float kMostWeight = 1.2379400392853803e27f;  // 2^90
 constexpr int kIB = 4;                              // per-item scratch buffers
 constexpr int kGroups = 2, kGroupWarps = 8;
 
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
         }
         linv[sg][r] = l > 0.f ? 1.f / l : 0.f;
         if (r < a.nh && !dead) {
-          if (!(l > 0.f && l <= 1152921504606846976.f) && atomicExch(a.flags + cur.row, 1) == 0)  // 2^60
+          if (!(l > 0.f && l <= kMostWeight) && atomicOr(a.flags + cur.row, 1 << ((a.h0 + r) >> 3)) == 0)
             a.flagged[atomicAdd(a.n_flagged, 1)] = cur.row;
           if (cur.part >= 0) {
             a.mpart[int64_t(cur.part) * a.H + a.h0 + r] = -neg_m[ib][r];

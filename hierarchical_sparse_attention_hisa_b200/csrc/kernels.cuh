@@ -99,12 +99,12 @@ struct TreeArgs {
   int4* items;                     // (first key row, first pair, pairs | key rows << 16, sequence << 3 | 128-row piece)
   int* counters;                   // [3]: items, pairs, flagged rows
   // the attention's work: items (row, first tile | tiles << 8 | kept rows << 16, part or -1 to write O whole, -)
-  // and each CTA's first; the rows that lie in several CTAs (row, first part, parts, -); and of each row whether
-  // its weights left the range of the fixed reference
+  // and each CTA's first; the rows that lie in several CTAs (row, first part, parts, -); and of each row the
+  // groups of eight heads (bits) whose weights left the range of the fixed reference
   int4* attn_items;
   int* cta_items;                  // [kTreeAttnCtas + 1]
   int4* cut;                       // [kTreeAttnCtas], row -1 behind the last
-  int *flags, *flagged;            // [rows] each: whether, and a list of those
+  int *flags, *flagged;            // [rows] each: the bits, and a list of the rows that have any
   uint16_t* O;                     // [rows][H][d]
   int H;
 };

@@ -375,77 +375,93 @@ __global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int64_
 }
 
 // One head of a row whose weights left the range that the attention's fixed
-// reference covers, on CUDA cores with a running maximum, by a warp: 128 kept
-// rows at a time, a lane scores four of them, then holds D / 32 output values.
-// (Out of line: the registers it needs would halve the CTAs of the combination.)
+// reference covers, on CUDA cores with a running maximum, by a warp: 32 kept
+// rows at a time, eight of them loaded at once, a lane holding D / 32 values of
+// each. (Out of line: the registers it needs would halve the combination's CTAs.)
 template <int D>
 __device__ __noinline__ void attend_head(const uint16_t* K, const uint16_t* V, const int32_t* idx, int n,
-                                         const uint16_t* q, float scale, float* p_s, uint16_t* out) {
-  constexpr int VPL = D / 32;
+                                         const uint16_t* q, float scale, uint16_t* out) {
+  constexpr int W = D / 64;  // 32-bit words per lane and row
   const int lane = threadIdx.x & 31;
-  float M = -INFINITY, l = 0.f, o[VPL] = {};
-  for (int c0 = 0; c0 < n; c0 += 128) {
-    float x[4], top = -INFINITY;
-    bool bad = false;
+  float qv[2 * W], o[2 * W] = {};
+#pragma unroll
+  for (int e = 0; e < W; ++e) {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(q)[lane * W + e];
+    qv[2 * e] = bf16_lo(w);
+    qv[2 * e + 1] = bf16_hi(w);
+  }
+  float M = -INFINITY, l = 0.f;
 #pragma unroll 1
-    for (int u = 0; u < 4; ++u) {
-      const int c = c0 + 32 * u + lane;
-      float acc = -INFINITY;
-      if (c < n) {
-        const uint4* kr = reinterpret_cast<const uint4*>(K + int64_t(max(idx[c], 0)) * D);
-        const uint4* qr = reinterpret_cast<const uint4*>(q);
-        acc = 0.f;
-#pragma unroll 2
-        for (int e = 0; e < D / 8; ++e) {
-          const uint4 kv = kr[e], qv = qr[e];
-          acc = __fmaf_rn(bf16_lo(qv.x), bf16_lo(kv.x), acc); acc = __fmaf_rn(bf16_hi(qv.x), bf16_hi(kv.x), acc);
-          acc = __fmaf_rn(bf16_lo(qv.y), bf16_lo(kv.y), acc); acc = __fmaf_rn(bf16_hi(qv.y), bf16_hi(kv.y), acc);
-          acc = __fmaf_rn(bf16_lo(qv.z), bf16_lo(kv.z), acc); acc = __fmaf_rn(bf16_hi(qv.z), bf16_hi(kv.z), acc);
-          acc = __fmaf_rn(bf16_lo(qv.w), bf16_lo(kv.w), acc); acc = __fmaf_rn(bf16_hi(qv.w), bf16_hi(kv.w), acc);
-        }
-        acc *= scale;
-        bad = bad || acc != acc;
+  for (int c0 = 0; c0 < n; c0 += 32) {
+    const int j = max(idx[min(c0 + lane, n - 1)], 0);
+    float x = -INFINITY;  // lane i: the score of row c0 + i
+#pragma unroll 1
+    for (int k0 = 0; k0 < 32; k0 += 8) {
+      uint32_t w[8][W];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t* r = reinterpret_cast<const uint32_t*>(K + int64_t(__shfl_sync(kFull, j, k0 + i)) * D) + lane * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[i][e] = r[e];
       }
-      p_s[32 * u + lane] = acc;
-      top = fmaxf(top, acc);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float acc = 0.f;
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          acc = __fmaf_rn(qv[2 * e], bf16_lo(w[i][e]), acc);
+          acc = __fmaf_rn(qv[2 * e + 1], bf16_hi(w[i][e]), acc);
+        }
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) acc += __shfl_xor_sync(kFull, acc, s);
+        if (lane == k0 + i && c0 + lane < n) x = acc * scale;
+      }
     }
+    float top = x;  // (the maximum leaves NaN out, the sum below does not)
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
     const float Mn = fmaxf(M, top), ref = Mn == -INFINITY ? 0.f : Mn;
-    const float g = M == -INFINITY ? 0.f : expf(M - ref);
-    float add = bad ? NAN : 0.f;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      x[u] = expf(p_s[32 * u + lane] - ref);
-      add += x[u];
-      p_s[32 * u + lane] = x[u];
-    }
+    const float g = M == -INFINITY ? 0.f : expf(M - ref), p = expf(x - ref);
+    float add = p;
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) add += __shfl_xor_sync(kFull, add, s);
     l = l * g + add;
     M = Mn;
 #pragma unroll
-    for (int e = 0; e < VPL; ++e) o[e] *= g;
-    __syncwarp();
+    for (int e = 0; e < 2 * W; ++e) o[e] *= g;
 #pragma unroll 1
-    for (int c = c0; c < min(n, c0 + 128); ++c) {
-      const float p = p_s[c - c0];
-      const uint16_t* vr = V + int64_t(max(idx[c], 0)) * D + lane * VPL;
+    for (int k0 = 0; k0 < 32; k0 += 8) {
+      uint32_t w[8][W];
 #pragma unroll
-      for (int e = 0; e < VPL; ++e) o[e] = __fmaf_rn(p, __uint_as_float(uint32_t(vr[e]) << 16), o[e]);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t* r = reinterpret_cast<const uint32_t*>(V + int64_t(__shfl_sync(kFull, j, k0 + i)) * D) + lane * W;
+#pragma unroll
+        for (int e = 0; e < W; ++e) w[i][e] = r[e];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float pi = __shfl_sync(kFull, p, k0 + i);
+        if (c0 + k0 + i >= n) break;  // (rows past the list repeat its last one)
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+          o[2 * e] = __fmaf_rn(pi, bf16_lo(w[i][e]), o[2 * e]);
+          o[2 * e + 1] = __fmaf_rn(pi, bf16_hi(w[i][e]), o[2 * e + 1]);
+        }
+      }
     }
-    __syncwarp();
   }
   // (every score -inf: no weights at all, as a row that keeps nothing)
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int e = 0; e < VPL; ++e) out[lane * VPL + e] = uint16_t(f32_to_bf16_rn(o[e] * inv));
+  for (int e = 0; e < W; ++e)
+    reinterpret_cast<uint32_t*>(out)[lane * W + e] = cvt_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
 }
 
 // O of the rows that were cut (with M the largest part maximum, O = sum_p
 // 2^(m_p - M) O_p / sum_p 2^(m_p - M) l_p in log2 units), and of the flagged
-// rows (taken again). Grid (cut, head groups), a thread per four values; the
-// parts come U at a time, every load of a group issued before any is used.
+// groups of eight heads (taken again). Grid (cut, head groups), a thread per four
+// values; the parts come U at a time, every load of a group issued before any is
+// used.
 template <int D, int U>
 __global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const TreeArgs a,
                                                                           const uint16_t* __restrict__ Q,
@@ -454,12 +470,11 @@ __global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const
                                                                           const float* __restrict__ mpart,
                                                                           const float* __restrict__ lpart) {
   constexpr int TPH = D / 4, HPC = 256 / TPH;  // threads per head, heads per CTA at a time
-  __shared__ float p_s[8][128];
   griddep_wait();
   griddep_launch();
   const int H = a.H, v = threadIdx.x % TPH;
   const int4 cut = a.cut[blockIdx.x];
-  const int skip = cut.x < 0 ? 1 : a.flags[cut.x];  // (its load is not waited for until a store)
+  const int flags = cut.x < 0 ? 0 : a.flags[cut.x];  // (its load is not waited for until a store)
   for (int h = blockIdx.y * HPC + threadIdx.x / TPH; cut.x >= 0 && h < H; h += gridDim.y * HPC) {
     float M = -INFINITY, den = 0.f;
     float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -490,7 +505,7 @@ __global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const
       }
     }
     const float inv = 1.f / den;
-    if (!skip)
+    if (!(flags >> (h >> 3) & 1))
       reinterpret_cast<uint2*>(a.O + (int64_t(cut.x) * H + h) * D)[v] =
           make_uint2(cvt_bf16x2(num.x * inv, num.y * inv), cvt_bf16x2(num.z * inv, num.w * inv));
   }
@@ -498,10 +513,11 @@ __global__ void __launch_bounds__(256, U == 4 ? 6 : 2) tree_combine_kernel(const
   for (int i = blockIdx.x; i < again; i += gridDim.x) {
     const int64_t row = a.flagged[i];
     const int64_t base = row / a.T * a.capacity * D;
-    const int n = min(a.k, candidates(a.rowpos[row], a.B, a.m));
+    const int n = min(a.k, candidates(a.rowpos[row], a.B, a.m)), bits = a.flags[row];
     for (int h = blockIdx.y * 8 + threadIdx.x / 32; h < H; h += gridDim.y * 8)
-      attend_head<D>(a.K_cache + base, a.V_cache + base, idx + row * a.k, n, Q + (row * H + h) * D, scale,
-                     p_s[threadIdx.x / 32], a.O + (row * H + h) * D);
+      if (bits >> (h >> 3) & 1)
+        attend_head<D>(a.K_cache + base, a.V_cache + base, idx + row * a.k, n, Q + (row * H + h) * D, scale,
+                       a.O + (row * H + h) * D);
   }
 }
 

@@ -224,8 +224,8 @@ STEP_CASES = {
     "wide_rows": dict(B=64, m=300, k=1000, d_idx=64, H=4, d=64, ctx=[30000, 20095], T=6, capacity=32768),
     "scaled": dict(SMALL, ctx=[900], T=6, capacity=1024, scale=0.7),
     # logits hundreds of nats apart: weights that leave the range of a list's first tile
-    "hot": dict(B=64, m=16, k=700, d_idx=64, H=20, d=64, ctx=[1900, 1500], T=9, capacity=2048, scale=8.0),
-    "hot_wide": dict(B=128, m=8, k=1000, d_idx=128, H=70, d=128, ctx=[1900, 1000], T=40, capacity=2048, scale=3.0),
+    "hot": dict(B=64, m=16, k=700, d_idx=64, H=20, d=64, ctx=[1900, 1500], T=9, capacity=2048, scale=14.0),
+    "hot_wide": dict(B=128, m=8, k=1000, d_idx=128, H=70, d=128, ctx=[1900, 1000], T=40, capacity=2048, scale=8.0),
     # 4 and 64 tiles of kept rows per node
     "long_lists": dict(B=128, m=64, k=8192, d_idx=64, H=3, d=128, ctx=[8190, 9000, 300], T=7, capacity=9216),
     # every score the same: ties go to the lowest position
