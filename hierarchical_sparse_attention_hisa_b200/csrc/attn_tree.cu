@@ -27,10 +27,11 @@
 // tiles, no later tile looks for another. That is exact to rounding as long as
 // nothing leaves the range of fp32 and bf16 exponents: weights may grow to 2^90
 // times the first tile's largest (62 nats above its maximum; 2^90 times values
-// below 2^37 still fits O). Where a head's sum passes 2^90, is not positive or not
-// a number, its group of eight heads is flagged, and taken again by
-// tree_combine_kernel with a running maximum, at some 40 times the cost. P is rounded to bf16 for the second MMA (2^-9 of each weight,
-// independent from key to key), everything else is fp32, O rounded once.
+// below 2^37 still fits O). Where a head's sum passes 2^90, is not positive or
+// not a number, its group of eight heads is flagged, and taken again by
+// tree_combine_kernel with a running maximum, at some 20 times the cost. P is
+// rounded to bf16 for the second MMA (2^-9 of each weight, independent from key
+// to key), everything else is fp32, O rounded once.
 //
 // Every mbarrier wait is bounded. A thread whose wait runs out goes on through
 // its loops without waiting (and without storing), so that named barriers and
