@@ -273,21 +273,151 @@ __global__ void __launch_bounds__(kFewNT) tree_few_scores_kernel(const TreeArgs 
 }
 
 // ---------------------------------------------------------------------------
-// Selections with a wide CTA per row, keys in registers (RegSelect): what a
-// step's latency needs, where the prefill's kernels are made for many rows (a
-// step of 8 nodes at 128K: 37.0 us, with 512 threads per top-k row 39.7, with
-// 256 49.0).
+// Selections with a wide CTA per row: what a step's latency needs, where the
+// prefill's kernels are made for many rows (a step of 8 nodes at 128K: 37.0 us,
+// with 512 threads per top-k row 39.7, with 256 49.0).
 //
-// Top-m: candidate c is block c + 1 of 1 .. nb-2; bkeys rows start three keys
-// in, so that block 1's key is on 16 bytes.
+// WideSelect picks the r largest of n keys (1 <= r < n <= 16384) held in
+// registers, thread t positions t*KPT .. t*KPT + KPT - 1, ties to the lowest
+// position. One histogram of 2048 bins linear in the score finds the bin of the
+// r-th largest; its keys, if at most 64, are ranked pairwise. A crowded bin (or
+// a range that is not finite) goes through RegSelect's rounds. Counts cross the
+// CTA by one value per warp that every warp sums for itself: five barriers, or
+// seven with a ranking, where the general selection takes some sixteen (top-k of
+// 8192 keys with its loads: 7.0 us before).
 // ---------------------------------------------------------------------------
 template <int NT, int KPT>
+struct __align__(16) WideSmem {
+  uint32_t hist[RegSelect<NT, KPT>::kBins];
+  uint32_t list[64];
+  int warp[3][NT / 32];
+  int pick[4];
+  int scratch[NT / 32 + 8];
+};
+
+template <int NT, int KPT>
+struct WideSelect {
+  static constexpr int NW = NT / 32, kBins = RegSelect<NT, KPT>::kBins, BPT = kBins / NT;
+  WideSmem<NT, KPT>& S;
+
+  // before the keys are there: no barrier, the first one in select() covers it
+  HSA_DEV void prepare() {
+#pragma unroll
+    for (int e = 0; e < BPT; ++e) S.hist[threadIdx.x * BPT + e] = 0;
+    if (threadIdx.x == 0) S.pick[2] = 0;
+  }
+
+  // The thread's selected keys as bits, and how many are selected at lower positions.
+  HSA_DEV uint32_t select(const uint32_t (&key)[KPT], int n, int r, int* before) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int have = max(0, min(KPT, n - int(threadIdx.x) * KPT));
+    uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j)
+      if (j < have) { lo = min(lo, key[j]); hi = max(hi, key[j]); }
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+    if (lane == 0) { S.warp[0][w] = int(lo); S.warp[1][w] = int(hi); }
+    __syncthreads();
+    lo = __reduce_min_sync(kFull, lane < NW ? uint32_t(S.warp[0][lane]) : 0xffffffffu);
+    hi = __reduce_max_sync(kFull, lane < NW ? uint32_t(S.warp[1][lane]) : 0u);
+    const float flo = key_score(lo), fhi = key_score(hi), c = float(kBins - 1) / (fhi - flo);
+    // A bin never decreases as the score grows (every step is monotone), so it is a range of keys. Adding 2^23
+    // leaves the rounded bin in the low bits: a conversion runs at a quarter of the rate.
+    auto vbin = [&](uint32_t u) {
+      return min(__float_as_uint(__fmaf_rn(key_score(u) - flo, c, 8388608.f)) - 0x4b000000u, uint32_t(kBins - 1));
+    };
+    // the r-th largest key, and how many of its equals are taken
+    uint32_t T = 0;
+    int take_eq = -1;
+    if (flo < fhi && c > 0.f && c < INFINITY) {
+#pragma unroll
+      for (int j = 0; j < KPT; ++j)
+        if (j < have) atomicAdd(&S.hist[vbin(key[j])], 1u);
+      __syncthreads();
+      int cnt[BPT], tot = 0;
+#pragma unroll
+      for (int e = 0; e < BPT; ++e) { cnt[e] = int(S.hist[threadIdx.x * BPT + e]); tot += cnt[e]; }
+      int x = tot;  // over the warp's lanes from this one on
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_down_sync(kFull, x, o);
+        if (lane + o < 32) x += y;
+      }
+      if (lane == 0) S.warp[2][w] = x;
+      __syncthreads();
+      int above = x - tot + int(__reduce_add_sync(kFull, lane < NW && lane > w ? unsigned(S.warp[2][lane]) : 0u));
+      if (above < r && r <= above + tot) {
+#pragma unroll
+        for (int e = BPT - 1; e >= 0; --e) {
+          if (above < r && r <= above + cnt[e]) { S.pick[0] = threadIdx.x * BPT + e; S.pick[1] = above; }
+          above += cnt[e];
+        }
+      }
+      __syncthreads();
+      const uint32_t bin = uint32_t(S.pick[0]);
+      const int rem = r - S.pick[1], in = int(S.hist[bin]);
+      if (in <= 64) {
+#pragma unroll
+        for (int j = 0; j < KPT; ++j)
+          if (j < have && vbin(key[j]) == bin) S.list[atomicAdd(&S.pick[2], 1)] = key[j];
+        __syncthreads();
+        if (int(threadIdx.x) < in) {
+          const uint32_t u = S.list[threadIdx.x];
+          int gt = 0, ge = 0;
+#pragma unroll 8
+          for (int q = 0; q < in; ++q) {
+            const uint32_t y = S.list[q];
+            gt += y > u;
+            ge += y >= u;
+          }
+          if (gt < rem && rem <= ge) { S.pick[0] = int(u); S.pick[3] = rem - gt; }  // writers agree
+        }
+        __syncthreads();
+        T = uint32_t(S.pick[0]);
+        take_eq = S.pick[3];
+      }
+    }
+    if (take_eq < 0) {  // (the whole CTA)
+      __syncthreads();
+      RegSelect<NT, KPT> rs{S.hist, S.scratch};
+      rs.threshold(key, n, r, &T, &take_eq);
+    }
+    uint32_t gt = 0, eq = 0;
+#pragma unroll
+    for (int j = 0; j < KPT; ++j) {
+      gt |= uint32_t(j < have && key[j] > T) << j;
+      eq |= uint32_t(j < have && key[j] == T) << j;
+    }
+    const int mine = __popc(gt) << 16 | __popc(eq);  // (both counts stay below 2^15)
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) S.warp[0][w] = incl;
+    __syncthreads();
+    const int at = incl - mine + int(__reduce_add_sync(kFull, lane < w ? unsigned(S.warp[0][lane]) : 0u));
+    const int gt_before = at >> 16, eq_before = at & 0xffff;
+    *before = gt_before + min(eq_before, take_eq);
+    for (int q = eq_before; eq && q < take_eq; eq &= eq - 1, ++q) gt |= eq & (0u - eq);
+    return gt;
+  }
+};
+
+// Top-m: candidate c is block c + 1 of 1 .. nb-2; bkeys rows start three keys
+// in, so that block 1's key is on 16 bytes.
+template <int NT, int KPT>
 __global__ void __launch_bounds__(NT) tree_topm_kernel(const TreeArgs a, int32_t* __restrict__ blocks) {
-  __shared__ uint32_t hist[RegSelect<NT, KPT>::kBins];
-  __shared__ int scratch[NT / 32 + 8];
+  __shared__ WideSmem<NT, KPT> S;
+  WideSelect<NT, KPT> sel{S};
+  sel.prepare();
   griddep_wait();
   griddep_launch();
   const int64_t row = blockIdx.x;
+  uint32_t key[KPT];  // (loaded beside the position: the row holds at least capacity / B - 1 keys)
+  load_keys<KPT>(a.bkeys + row * a.ldb + kBkeys0 + 1, int(a.ldb) - kBkeys0 - 1, key);
   const int64_t t = a.rowpos[row];
   int32_t* out = blocks + row * a.m;
   const int64_t nb = t < 0 ? 0 : t / a.B + 1;
@@ -297,42 +427,38 @@ __global__ void __launch_bounds__(NT) tree_topm_kernel(const TreeArgs a, int32_t
   }
   if (threadIdx.x == 0) { out[0] = 0; out[a.m - 1] = int32_t(nb - 1); }
   if (a.m == 2) return;
-  const int n = int(nb - 2);
-  uint32_t key[KPT];
-  load_keys<KPT>(a.bkeys + row * a.ldb + kBkeys0 + 1, n, key);
-  RegSelect<NT, KPT> rs{hist, scratch};
-  uint32_t T;
-  int take_eq;
-  rs.threshold(key, n, a.m - 2, &T, &take_eq);
-  rs.compact(key, n, T, take_eq, [&](int rank, int c) { out[1 + rank] = c + 1; });
+  int at;
+  uint32_t bits = sel.select(key, int(nb - 2), a.m - 2, &at);
+  for (; bits; bits &= bits - 1) out[1 + at++] = threadIdx.x * KPT + __ffs(bits);
 }
 
 // Top-k of a node's candidates (the tokens of its kept blocks, ascending), and
-// their positions as rows of the sequence's cache.
+// their positions as rows of the sequence's cache; up to 2048 are gathered over
+// the histogram and written out whole. (A buffer of its own for more would keep
+// the attention's CTA from being set up beside this one.)
 template <int NT, int KPT>
 __global__ void __launch_bounds__(NT, NT == 1024 && KPT <= 8 ? 2 : 1) tree_topk_kernel(const TreeArgs a,
                                                                                       int32_t* __restrict__ idx) {
-  __shared__ uint32_t hist[RegSelect<NT, KPT>::kBins];
-  __shared__ int scratch[NT / 32 + 8];
+  __shared__ WideSmem<NT, KPT> S;
   __shared__ int blk[512];
   __shared__ int path[kTreeMax];
+  WideSelect<NT, KPT> sel{S};
+  sel.prepare();
   griddep_wait();
   griddep_launch();
   const int64_t row = blockIdx.x;
-  const int64_t t = a.rowpos[row];
+  // every load at once; keys behind the row's candidates are not looked at
+  uint32_t key[KPT];
+  load_keys<KPT>(a.tkeys + row * int64_t(a.m) * a.B, a.m * a.B, key);
+  const int t = a.rowpos[row], c0 = a.ctx[row / a.T];
+  for (int s = threadIdx.x; s < a.m; s += NT) blk[s] = a.blocks[row * a.m + s];
+  if (int(threadIdx.x) < a.T) path[threadIdx.x] = min(max(a.paths[row * a.T + threadIdx.x], 0), a.T - 1);
   int32_t* out = idx + row * a.k;
   if (t < 0) {
     for (int s = threadIdx.x; s < a.k; s += NT) out[s] = -1;
     return;
   }
-  const int n = candidates(int(t), a.B, a.m);
-  uint32_t key[KPT];
-  if (n > a.k) load_keys<KPT>(a.tkeys + row * int64_t(a.m) * a.B, n, key);
-  for (int s = threadIdx.x; s < a.m; s += NT) blk[s] = a.blocks[row * a.m + s];
-  const int c0 = a.ctx[row / a.T];
-  if (int(threadIdx.x) <= int(t) - c0)
-    path[threadIdx.x] = min(max(a.paths[row * a.T + threadIdx.x], 0), a.T - 1);
-  __syncthreads();
+  const int n = candidates(t, a.B, a.m);
   const bool pow2 = (a.B & (a.B - 1)) == 0;
   const int lb = 31 - __clz(a.B);
   auto row_of = [&](int c) -> int32_t {
@@ -340,14 +466,21 @@ __global__ void __launch_bounds__(NT, NT == 1024 && KPT <= 8 ? 2 : 1) tree_topk_
     return p < c0 ? p : c0 + path[p - c0];
   };
   if (n <= a.k) {
+    __syncthreads();
     for (int s = threadIdx.x; s < a.k; s += NT) out[s] = s < n ? row_of(s) : -1;
     return;
   }
-  RegSelect<NT, KPT> rs{hist, scratch};
-  uint32_t T;
-  int take_eq;
-  rs.threshold(key, n, a.k, &T, &take_eq);
-  rs.compact(key, n, T, take_eq, [&](int rank, int c) { out[rank] = row_of(c); });
+  int at;
+  uint32_t bits = sel.select(key, n, a.k, &at);
+  int32_t* kept = a.k <= int(sizeof(S.hist) / 4) ? reinterpret_cast<int32_t*>(S.hist) : out;
+  for (; bits; bits &= bits - 1) kept[at++] = row_of(threadIdx.x * KPT + __ffs(bits) - 1);
+  if (kept == out) return;
+  __syncthreads();
+  if ((a.k & 3) == 0) {
+    for (int e = threadIdx.x; e < a.k / 4; e += NT) reinterpret_cast<int4*>(out)[e] = reinterpret_cast<const int4*>(kept)[e];
+  } else {
+    for (int e = threadIdx.x; e < a.k; e += NT) out[e] = kept[e];
+  }
 }
 
 // Kept positions of each node -> rows of its sequence's cache, in place, a warp
