@@ -110,9 +110,9 @@ struct TreeArgs {
 };
 constexpr int kTreeAttnCtas = 148;  // one per SM
 constexpr int kBkeys0 = 3;          // so that block 1's key, the first candidate, is on 16 bytes
-// Rows up to which the wide top-k is taken. Against the prefill's kernel and the mapping launch: 8.8 and 14.3 us
-// for 8 rows, 14.5 and 16.0 for 512; a whole step of 608 rows 142 and 140 us, of 1024 rows 200 and 194.
-constexpr int kWideRows = 592;
+// Rows up to which the wide top-k is taken: one wave of two CTAs per SM. Against the prefill's kernel and the
+// mapping launch, a whole step of 8 rows 34.8 and 42.7 us, of 512 rows 143.5 and 142.3, of 1024 rows 200 and 194.
+constexpr int kWideRows = 296;
 // Token candidates of a query at position t: all up to it, or those of its m kept blocks.
 HSA_DEV int candidates(int t, int B, int m) { return t / B < m ? t + 1 : (m - 1) * B + t % B + 1; }
 void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, const int32_t* n_nodes,

@@ -274,8 +274,8 @@ __global__ void __launch_bounds__(kFewNT) tree_few_scores_kernel(const TreeArgs 
 
 // ---------------------------------------------------------------------------
 // Selections with a wide CTA per row: what a step's latency needs, where the
-// prefill's kernels are made for many rows (a step of 8 nodes at 128K: 37.0 us,
-// with 512 threads per top-k row 39.7, with 256 49.0).
+// prefill's kernels are made for many rows (a step of 8 nodes at 128K with 1024,
+// 512 and 256 threads per top-k row: 34.8, 35.6 and 38.9 us).
 //
 // WideSelect picks the r largest of n keys (1 <= r < n <= 16384) held in
 // registers, thread t positions t*KPT .. t*KPT + KPT - 1, ties to the lowest
