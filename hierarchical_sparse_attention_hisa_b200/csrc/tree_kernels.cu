@@ -83,32 +83,30 @@ __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
     const int t = a.rowpos[row];
     return t < 0 ? 0 : min(a.k, candidates(t, a.B, a.m));
   };
-  int mine = 0, total;  // (at most 64 tiles per row, 2^31 / m rows)
-#pragma unroll 4
-  for (int64_t row = r0; row < r1; ++row) mine += (kept_of(row) + 127) / 128;
+  const int kept0 = r0 < r1 ? kept_of(r0) : 0;  // (mostly the only one)
+  int mine = (kept0 + 127) / 128, total;          // (at most 64 tiles per row, rows below 2^25)
+  for (int64_t row = r0 + 1; row < r1; ++row) mine += (kept_of(row) + 127) / 128;
   const int tile0 = block_exclusive_scan<NT>(mine, s_tmp, &total);
   const int quota = max(1, (total + kTreeAttnCtas - 1) / kTreeAttnCtas);
   // f(row, kept rows, first tile, tiles, pieces): a row's tiles lie in `pieces` CTAs
   auto for_rows = [&](auto fn) {
     int s = tile0;
-#pragma unroll 4
     for (int64_t row = r0; row < r1; ++row) {
-      const int kept = kept_of(row), n = (kept + 127) / 128;
+      const int kept = row == r0 ? kept0 : kept_of(row), n = (kept + 127) / 128;
       fn(row, kept, s, n, n ? (s + n - 1) / quota - s / quota + 1 : 0);
       s += n;
     }
   };
-  int items = 0, parts = 0, cuts = 0;
+  int items = 0, cuts = 0;  // cuts: pieces of cut rows << 16 | cut rows (at most 2 and 1 per CTA)
   for_rows([&](int64_t row, int, int, int, int pieces) {
     a.flags[row] = 0;
     items += pieces;
-    parts += pieces > 1 ? pieces : 0;
-    cuts += pieces > 1;
+    cuts += pieces > 1 ? pieces << 16 | 1 : 0;
   });
-  int all_items, all_parts, all_cuts;
+  int all_items, all_cuts;
   int at = block_exclusive_scan<NT>(items, s_tmp, &all_items);
-  int part = block_exclusive_scan<NT>(parts, s_tmp, &all_parts);
-  int cut = block_exclusive_scan<NT>(cuts, s_tmp, &all_cuts);
+  const int before = block_exclusive_scan<NT>(cuts, s_tmp, &all_cuts);
+  int part = before >> 16, cut = before & 0xffff;
   for_rows([&](int64_t row, int kept, int s, int n, int pieces) {
     if (pieces > 1) a.cut[cut++] = make_int4(int(row), part, pieces, 0);
     const int c0 = s / quota;
@@ -120,7 +118,7 @@ __device__ void attn_shares(const TreeArgs& a, int64_t rows, int* s_tmp) {
   });
   for (int c = (total + quota - 1) / quota + tid; c <= kTreeAttnCtas; c += NT) a.cta_items[c] = all_items;
   // (a cut lies between two CTAs, so fewer rows than CTAs are cut)
-  for (int c = all_cuts + tid; c < kTreeAttnCtas; c += NT) a.cut[c] = make_int4(-1, 0, 0, 0);
+  for (int c = (all_cuts & 0xffff) + tid; c < kTreeAttnCtas; c += NT) a.cut[c] = make_int4(-1, 0, 0, 0);
 }
 
 __device__ void tail_keys(const TreeArgs& a, int64_t row) {  // a warp per node
