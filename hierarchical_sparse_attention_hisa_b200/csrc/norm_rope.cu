@@ -265,7 +265,11 @@ void launch_qk_norm_rope(int64_t L, int H, int d, const void* Q, int64_t q_strid
   const int64_t by_group = (L + G - 1) / G;
   if (Q) {
     a.q = Side{(const uint16_t*)Q, (const uint16_t*)qw, (uint16_t*)Qo, q_stride, H, 0, 0, by_group};
-    if (H >= G) {
+    // A token to a warp (its angles computed once) from G heads on; with up to 1.5 G
+    // its second step leaves groups idle, and many tokens are better one to each group:
+    // 65,536 of 4 heads of 128 in 35.5 us (a warp each: 60), of 8 of 64 in 35 (52);
+    // 512 tokens take 2.9 us (a warp each: 2.5). At 2 G: 58 to 60 us either way.
+    if (H >= G && (2 * H > 3 * G || L < 16 * int64_t(num_sms()))) {
       // few tokens: their heads over more warps, down to 4 rows per group
       const int64_t want = std::min<int64_t>(std::max(1, H / (4 * G)), 16 * int64_t(num_sms()) / L);
       a.q.heads = (H + std::max<int64_t>(1, want) - 1) / std::max<int64_t>(1, want);

@@ -66,6 +66,9 @@ def hsa():
     (33, 64, 128, 128, False), (5, 64, 128, 64, True), (257, 4, 64, 64, True), (1000, 5, 64, 48, False),
     (1000, 16, 128, 96, False), (300, 3, 128, 80, True), (77, 1, 64, 32, False), (129, 128, 64, 0, False),
     (513, 31, 128, 112, False), (4099, 1, 128, 128, False),
+    # a token to a group or to a warp, on both sides of the choice
+    (2367, 4, 128, 128, False), (2371, 4, 128, 128, True), (2369, 6, 128, 48, False), (2500, 7, 128, 128, False),
+    (2401, 11, 64, 64, True), (2403, 12, 64, 32, False), (2405, 13, 64, 64, False),
 ])
 @pytest.mark.parametrize("fused", [False, True])
 def test_against_formula(hsa, L, H, d, rot, inter, fused):
