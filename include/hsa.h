@@ -253,7 +253,7 @@ HSA_API int hsa_decode_step_noalloc(const hsa_params* p, int32_t batch, int64_t 
  *   pairs (a, b) of y's first `rot` values turned by u = position * inv_freq[i]:
  *   (a cos u - b sin u, b cos u + a sin u); pair i is (i, i + rot/2), or
  *   (2i, 2i + 1) with interleaved = 1. The other values stay as they are.
- * fp32 throughout (u in fp64), rounded once to bf16.
+ * fp32 throughout (u taken in 64 bits), rounded once to bf16.
  *   Q      [L][H][d] bf16, token rows q_stride values apart (a multiple of 8,
  *          >= H*d: e.g. the rows of a fused projection), or NULL: keys only;
  *   K      [L][d] bf16, rows k_stride apart (a multiple of 8, >= d), or NULL:
