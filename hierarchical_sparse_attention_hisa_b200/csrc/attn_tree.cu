@@ -26,10 +26,11 @@
 // Softmax: the maximum of an item's first tile is the reference of all its
 // tiles, no later tile looks for another. That is exact to rounding as long as
 // nothing leaves the range of fp32 and bf16 exponents: weights may grow to 2^90
-// times the first tile's largest (62 nats above its maximum; 2^90 times values
-// below 2^37 still fits O). Where a head's sum passes 2^90, is not positive or
-// not a number, its group of eight heads is flagged, and taken again by
-// tree_combine_kernel with a running maximum, at some 20 times the cost. P is
+// times the first tile's largest (62 nats above its maximum), and their products
+// with V to 2^119 (a row's 64 parts at that size still add up below 2^128). Where
+// a head's sum passes 2^90, is not positive or not a number, or a value of its O
+// passes 2^119 or is not a number, its group of eight heads is flagged, and taken
+// again by tree_combine_kernel with a running maximum, at some 20 times the cost. P is
 // rounded to bf16 for the second MMA (2^-9 of each weight, independent from key
 // to key), everything else is fp32, O rounded once.
 //
@@ -52,6 +53,7 @@ constexpr int TILE = 128;
 constexpr long long kInjectWaitCycles = 1ll << 21;  // about a millisecond
 constexpr int kSB = 4, kOB = 2;                     // S and O buffers in TMEM
 constexpr float kMostWeight = 1.2379400392853803e27f;  // 2^90
+constexpr uint32_t kMostOut = (127u + 119u) << 23;     // 2^119, as the bits of an fp32
 constexpr int kIB = 4;                              // per-item scratch buffers
 constexpr int kGroups = 2, kGroupWarps = 8;
 
@@ -98,6 +100,11 @@ struct Args {
   float *Opart, *mpart, *lpart;
   int *flags, *flagged, *n_flagged;
 };
+
+// A group of eight heads of a row is to be taken again; a row's first group lists it.
+HSA_DEV void flag_heads(const Args& a, int row, int head) {
+  if (atomicOr(a.flags + row, 1 << (head >> 3)) == 0) a.flagged[atomicAdd(a.n_flagged, 1)] = row;
+}
 
 // Bounded wait. A failed probe goes straight back to the barrier: the limit,
 // the error flag and the test hook are global or slow to read, and a look at
@@ -469,8 +476,7 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
         }
         linv[sg][r] = l > 0.f ? 1.f / l : 0.f;
         if (r < a.nh && !dead) {
-          if (!(l > 0.f && l <= kMostWeight) && atomicOr(a.flags + cur.row, 1 << ((a.h0 + r) >> 3)) == 0)
-            a.flagged[atomicAdd(a.n_flagged, 1)] = cur.row;
+          if (!(l > 0.f && l <= kMostWeight)) flag_heads(a, cur.row, a.h0 + r);
           if (cur.part >= 0) {
             a.mpart[int64_t(cur.part) * a.H + a.h0 + r] = -neg_m[ib][r];
             a.lpart[int64_t(cur.part) * a.H + a.h0 + r] = l;
@@ -490,11 +496,18 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
           if (lane == 0) mbar_arrive(&bars.oempty[ob]);
         }
         if (r < DH && !dead) {
+#pragma unroll
+          for (int e = 0; e < CW; e += 8) {  // (as integers, magnitudes order with NaN above all)
+            uint32_t most = 0;
+#pragma unroll
+            for (int z = 0; z < 8; ++z) most = max(most, __float_as_uint(x[e + z]) & 0x7fffffffu);
+            if (most > kMostOut && h0 + c + e < a.nh) flag_heads(a, cur.row, a.h0 + h0 + c + e);
+          }
           if (cur.part < 0) {
             uint16_t* o = a.O + (int64_t(cur.row) * a.H + a.h0 + h0 + c) * DH + r;
 #pragma unroll
             for (int e = 0; e < CW; ++e)
-              if (h0 + c + e < a.nh) o[e * DH] = uint16_t(f32_to_bf16_rn(x[e] * linv[sg][h0 + c + e]));
+              if (h0 + c + e < a.nh) o[e * DH] = cvt_bf16(x[e] * linv[sg][h0 + c + e]);
           } else {
             float* o = a.Opart + (int64_t(cur.part) * a.H + a.h0 + h0 + c) * DH + r;
 #pragma unroll

@@ -26,6 +26,12 @@ HSA_DEV uint32_t cvt_bf16x2(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// One value of an output. (f32_to_bf16_rn would make a zero of a NaN.)
+HSA_DEV uint16_t cvt_bf16(float f) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(f));
+  return r;
+}
 
 // Order-preserving unsigned key of an fp32 score: larger score -> larger key.
 // -0 is folded onto +0 so that the two compare equal, as floats do.

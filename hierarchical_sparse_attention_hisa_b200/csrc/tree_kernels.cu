@@ -508,7 +508,9 @@ __global__ void __launch_bounds__(256) tree_rows_kernel(const TreeArgs a, int64_
 // One head of a row whose weights left the range that the attention's fixed
 // reference covers, on CUDA cores with a running maximum, by a warp: 32 kept
 // rows at a time, eight of them loaded at once, a lane holding D / 32 values of
-// each. (Out of line: the registers it needs would halve the combination's CTAs.)
+// each. Weights are held times 2^-13, so that 8192 of them times the largest
+// values stay in range. (Out of line: the registers it needs would halve the
+// combination's CTAs.)
 template <int D>
 __device__ __noinline__ void attend_head(const uint16_t* K, const uint16_t* V, const int32_t* idx, int n,
                                          const uint16_t* q, float scale, uint16_t* out) {
@@ -552,7 +554,7 @@ __device__ __noinline__ void attend_head(const uint16_t* K, const uint16_t* V, c
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, s));
     const float Mn = fmaxf(M, top), ref = Mn == -INFINITY ? 0.f : Mn;
-    const float g = M == -INFINITY ? 0.f : expf(M - ref), p = expf(x - ref);
+    const float g = M == -INFINITY ? 0.f : expf(M - ref), p = expf(x - ref) * 1.220703125e-4f;
     float add = p;
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) add += __shfl_xor_sync(kFull, add, s);
