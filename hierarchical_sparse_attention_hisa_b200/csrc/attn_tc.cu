@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
         if (orow) {
 #pragma unroll
           for (int h = 0; h < HH; ++h) {
-            if (h0 + h < nh && r < DH) orow[(h0 + h) * DH + r] = uint16_t(f32_to_bf16_rn(ov[h] * linv[h0 + h]));
+            if (h0 + h < nh && r < DH) orow[(h0 + h) * DH + r] = cvt_bf16(ov[h] * linv[h0 + h]);
           }
         } else {
           // one part of a split query: unnormalised O^T, running maximum, row sum

@@ -190,7 +190,7 @@ __global__ void decode_combine_kernel(int32_t* __restrict__ ctx, int64_t capacit
     }
     out = den > 0.f ? num / den : 0.f;
   }
-  O[(b * H + h) * D + threadIdx.x] = uint16_t(f32_to_bf16_rn(out));
+  O[(b * H + h) * D + threadIdx.x] = cvt_bf16(out);
   // every earlier kernel of the step has finished reading the lengths: the
   // sequence grows by one token
   if (h == 0 && threadIdx.x == 0) {
