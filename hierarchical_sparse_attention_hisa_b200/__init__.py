@@ -30,6 +30,41 @@ def _check_bf16(name, t, ndim):
         raise ValueError(f"{name}: expected a contiguous {ndim}-d bf16 CUDA tensor")
 
 
+class _On:
+    """Allocations and fills of a call that runs on `stream` (None: the current one) belong to that stream.
+
+    Made on the current stream instead, a fill would not be ordered with the call's kernels, and a workspace, given
+    back when the call returns, could be handed out again while they run.
+    """
+
+    def __init__(self, stream, device):
+        import torch
+        self.ctx = self.caller = None
+        if stream is None:
+            return
+        if not hasattr(stream, "cuda_stream"):  # a raw handle
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError("the stream is not on the tensors' device")
+        self.caller = torch.cuda.current_stream(device)
+        self.ctx = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.ctx:
+            self.ctx.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.ctx:
+            self.ctx.__exit__(*exc)
+
+    def result(self, t):
+        """A tensor that the caller will use on its own current stream, too."""
+        if self.ctx and t is not None:
+            t.record_stream(self.caller)
+        return t
+
+
 def index(q_idx, k_idx, B: int, m: int, k: int, stream=None):
     """indices [Lq][k] int32 for queries at positions Lk-Lq .. Lk-1."""
     import torch
@@ -38,11 +73,12 @@ def index(q_idx, k_idx, B: int, m: int, k: int, stream=None):
     Lq, d_idx = q_idx.shape
     Lk = k_idx.shape[0]
     p = params(B=B, m=m, k=k, d_idx=d_idx)
-    ws = torch.empty(max(hsa_index_workspace_size(p, Lq, Lk), 16), dtype=torch.uint8,
-                     device=q_idx.device)
-    out = torch.empty((Lq, k), dtype=torch.int32, device=q_idx.device)
-    hsa_index(p, Lq, Lk, q_idx, k_idx, out, ws, stream)
-    return out
+    with _On(stream, q_idx.device) as on:
+        ws = torch.empty(max(hsa_index_workspace_size(p, Lq, Lk), 16), dtype=torch.uint8,
+                         device=q_idx.device)
+        out = torch.empty((Lq, k), dtype=torch.int32, device=q_idx.device)
+        hsa_index(p, Lq, Lk, q_idx, k_idx, out, ws, stream)
+    return on.result(out)
 
 
 def sparse_attn(Q, K, V, indices, scale: float = 0.0, stream=None):
@@ -53,9 +89,10 @@ def sparse_attn(Q, K, V, indices, scale: float = 0.0, stream=None):
     _check_bf16("V", V, 2)
     Lq, H, d = Q.shape
     p = params(k=indices.shape[1], H=H, d=d, scale=scale)
-    O = torch.empty_like(Q)
-    hsa_sparse_attn(p, Lq, K.shape[0], Q, K, V, indices, O, stream)
-    return O
+    with _On(stream, Q.device) as on:
+        O = torch.empty_like(Q)
+        hsa_sparse_attn(p, Lq, K.shape[0], Q, K, V, indices, O, stream)
+    return on.result(O)
 
 
 def qk_norm_rope(Q, K, q_weight=None, k_weight=None, inv_freq=None, positions=None, pos0: int = 0,
@@ -64,7 +101,8 @@ def qk_norm_rope(Q, K, q_weight=None, k_weight=None, inv_freq=None, positions=No
 
     Q and K may be rows of a wider projection (only a token's own values must be
     contiguous); either may be None. Row i is at positions[i] (int32) or pos0 + i.
-    Rows with a negative position come back as zeros.
+    Rows with a negative position come back as zeros. With a stream given, the inputs must be ready on it, and
+    its work must be awaited before the results are used elsewhere.
     """
     import torch
     ref = Q if Q is not None else K
@@ -87,9 +125,10 @@ def qk_norm_rope(Q, K, q_weight=None, k_weight=None, inv_freq=None, positions=No
     H = Q.shape[1] if Q is not None else 1
     rot = 2 * inv_freq.numel() if inv_freq is not None else 0
     new = torch.empty if positions is None else torch.zeros
-    Qo = new((L, H, d), dtype=torch.bfloat16, device=ref.device) if Q is not None else None
-    Ko = new((L, d), dtype=torch.bfloat16, device=ref.device) if K is not None else None
-    if L:
-        hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, interleaved, positions, pos0, Qo, Ko,
-                         stream)
-    return Qo, Ko
+    with _On(stream, ref.device) as on:
+        Qo = new((L, H, d), dtype=torch.bfloat16, device=ref.device) if Q is not None else None
+        Ko = new((L, d), dtype=torch.bfloat16, device=ref.device) if K is not None else None
+        if L:
+            hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, interleaved, positions, pos0, Qo,
+                             Ko, stream)
+    return on.result(Qo), on.result(Ko)
