@@ -9,6 +9,7 @@ ImportError, never a silent fallback.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 from . import build as _build
@@ -215,20 +216,41 @@ def hsa_decode_step_noalloc(p, batch, capacity, ctx_len, k_idx_cache, K_cache, V
         _p(V_new), _p(O), _p(indices_out), _s(stream)))
 
 
+def _token_stride(name, t, L, H, d):
+    """Values from one token of t to the next: t is [tokens ...][heads][d], or [tokens ...][d] where H = 1."""
+    shape, st = t.shape, t.stride()
+    if st[-1] != 1 or (H > 1 and st[-2] != d):
+        raise ValueError(f"{name}: the {'heads of a token' if H > 1 else 'values of a row'} must be contiguous")
+    last = len(shape) - 1  # the dimensions before this one are tokens
+    if H > 1 or (last > 1 and math.prod(shape[:-2]) >= L):
+        last -= 1
+    n, stride = 1, H * d
+    for i in range(last - 1, -1, -1):
+        if shape[i] == 1:
+            continue
+        if n == 1:
+            stride = st[i]
+        elif st[i] != n * stride:
+            raise ValueError(f"{name}: the tokens must be a fixed stride apart")
+        n *= shape[i]
+    if n < L:
+        raise ValueError(f"{name}: {n} tokens, expected {L}")
+    return stride if L > 1 else H * d
+
+
 def hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, interleaved, positions, pos0,
                      Q_out, K_out, stream=None):
-    """Row strides are the tensors' own; a token's heads and values must be contiguous."""
+    """Row strides are the tensors' own; a token's heads and values must be contiguous. Tokens may span several
+    dimensions ([batch][T][H][d]) as long as they are a fixed stride apart."""
     q_stride = k_stride = 0
     if Q is not None:
         st = Q.stride()
-        if st[-1] != 1 or (H > 1 and st[-2] != d):
-            raise ValueError("Q: the heads of a token must be contiguous")
-        q_stride = st[0] if L > 1 else H * d
+        usual = len(st) == 3 and st[2] == 1 and st[1] == d and 1 < L <= Q.size(0)
+        q_stride = st[0] if usual else _token_stride("Q", Q, L, H, d)
     if K is not None:
         st = K.stride()
-        if st[-1] != 1:
-            raise ValueError("K: the values of a row must be contiguous")
-        k_stride = st[0] if L > 1 else d
+        usual = len(st) == 2 and st[1] == 1 and 1 < L <= K.size(0)
+        k_stride = st[0] if usual else _token_stride("K", K, L, 1, d)
     st = (_lib or load()).hsa_qk_norm_rope(
         L, H, d, _p(Q), q_stride, _p(K), k_stride, _p(q_weight), _p(k_weight), eps, _p(inv_freq), rot,
         1 if interleaved else 0, _p(positions), pos0, _p(Q_out), _p(K_out), _s(stream))
