@@ -251,6 +251,9 @@ def hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, inte
         st = K.stride()
         usual = len(st) == 2 and st[1] == 1 and 1 < L <= K.size(0)
         k_stride = st[0] if usual else _token_stride("K", K, L, 1, d)
+    if (Q is not None and Q_out is not None and not Q_out.is_contiguous()) or \
+            (K is not None and K_out is not None and not K_out.is_contiguous()):
+        raise ValueError("Q_out and K_out must be contiguous")
     st = (_lib or load()).hsa_qk_norm_rope(
         L, H, d, _p(Q), q_stride, _p(K), k_stride, _p(q_weight), _p(k_weight), eps, _p(inv_freq), rot,
         1 if interleaved else 0, _p(positions), pos0, _p(Q_out), _p(K_out), _s(stream))

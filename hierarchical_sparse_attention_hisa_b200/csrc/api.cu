@@ -425,7 +425,7 @@ extern "C" int hsa_qk_norm_rope(int64_t L, int32_t H, int32_t d, const hsa_bf16*
   if (!Q && !K) return HSA_ERR_ARG;
   auto rows_ok = [&](const hsa_bf16* in, const hsa_bf16* w, const hsa_bf16* out, int64_t stride, int64_t n) {
     return aligned16(in) && aligned16(out) && (!w || aligned16(w)) && stride >= n && stride % 8 == 0 &&
-           stride <= (int64_t(1) << 62) / L;
+           stride <= (int64_t(1) << 62) / L && (in != out || stride == n || L == 1);  // in place: dense rows only
   };
   if (Q && !rows_ok(Q, q_weight, Q_out, q_stride, int64_t(H) * d)) return HSA_ERR_ARG;
   if (K && !rows_ok(K, k_weight, K_out, k_stride, d)) return HSA_ERR_ARG;

@@ -265,7 +265,8 @@ HSA_API int hsa_decode_step_noalloc(const hsa_params* p, int32_t batch, int64_t 
  *          hsa_tree_plan for a drafted tree), or NULL: row i is at pos0 + i.
  *          A row with a negative position is left unwritten;
  *   Q_out  [L][H][d], K_out [L][d] bf16, dense. Each may be its input if that
- *          is dense too; otherwise outputs must not overlap inputs.
+ *          is dense too (refused if it is not); otherwise outputs must not
+ *          overlap inputs.
  * pos0 >= 0 and pos0 + L < 2^31 (ignored with positions). One launch. */
 HSA_API int hsa_qk_norm_rope(int64_t L, int32_t H, int32_t d, const hsa_bf16* Q, int64_t q_stride,
                              const hsa_bf16* K, int64_t k_stride, const hsa_bf16* q_weight,
