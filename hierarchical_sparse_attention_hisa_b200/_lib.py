@@ -263,8 +263,7 @@ def hsa_qk_norm_rope(L, H, d, Q, K, q_weight, k_weight, eps, inv_freq, rot, inte
 
 def hsa_tree_plan(batch, T, capacity, ctx_len, n_nodes, parents, positions, paths, stream=None):
     st = (_lib or load()).hsa_tree_plan(
-        batch, T, capacity, ctx_len.data_ptr(), _p(n_nodes), parents.data_ptr(), positions.data_ptr(),
-        paths.data_ptr(), _s(stream))
+        batch, T, capacity, _p(ctx_len), _p(n_nodes), _p(parents), _p(positions), _p(paths), _s(stream))
     if st:
         raise HSAError("hsa_tree_plan", st)
 
@@ -279,11 +278,10 @@ def hsa_tree_workspace_size(p, batch, T, capacity) -> int:
 def hsa_tree_step(p, batch, T, capacity, ctx_len, positions, paths, k_idx_cache, K_cache, V_cache, ksum_cache,
                   q_idx_new, k_idx_new, Q_new, K_new, V_new, O, indices_out, workspace, stream=None):
     st = (_lib or load()).hsa_tree_step(
-        ctypes.byref(p), batch, T, capacity, ctx_len.data_ptr(), positions.data_ptr(), paths.data_ptr(),
-        k_idx_cache.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), ksum_cache.data_ptr(),
-        q_idx_new.data_ptr(), k_idx_new.data_ptr(), Q_new.data_ptr(), K_new.data_ptr(), V_new.data_ptr(),
-        O.data_ptr(), _p(indices_out), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _s(stream))
+        ctypes.byref(p), batch, T, capacity, _p(ctx_len), _p(positions), _p(paths), _p(k_idx_cache), _p(K_cache),
+        _p(V_cache), _p(ksum_cache), _p(q_idx_new), _p(k_idx_new), _p(Q_new), _p(K_new), _p(V_new), _p(O),
+        _p(indices_out), _p(workspace),
+        workspace.numel() * workspace.element_size() if workspace is not None else 0, _s(stream))
     if st:
         raise HSAError("hsa_tree_step", st)
 
@@ -291,7 +289,7 @@ def hsa_tree_step(p, batch, T, capacity, ctx_len, positions, paths, k_idx_cache,
 def hsa_tree_commit(p, batch, T, capacity, ctx_len, paths, accepted, k_idx_cache, K_cache, V_cache, ksum_cache,
                     stream=None):
     st = (_lib or load()).hsa_tree_commit(
-        ctypes.byref(p), batch, T, capacity, ctx_len.data_ptr(), paths.data_ptr(), accepted.data_ptr(),
-        k_idx_cache.data_ptr(), K_cache.data_ptr(), V_cache.data_ptr(), ksum_cache.data_ptr(), _s(stream))
+        ctypes.byref(p), batch, T, capacity, _p(ctx_len), _p(paths), _p(accepted), _p(k_idx_cache), _p(K_cache),
+        _p(V_cache), _p(ksum_cache), _s(stream))
     if st:
         raise HSAError("hsa_tree_commit", st)
