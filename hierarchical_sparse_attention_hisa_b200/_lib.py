@@ -118,18 +118,28 @@ def _p(t):
     return None if t is None else t.data_ptr() or None
 
 
-def _current():
-    """Handle of the current device's current stream (rebound on first use: a Stream object costs 1 us a call)."""
-    global _current
+def _stream_source():
+    """A function that gives the handle of the current device's current stream (a Stream object costs 1 us a call).
+
+    The raw handle comes from functions that torch does not document; without them, from torch.cuda.current_stream().
+    """
     import torch
     torch.cuda.init()
-    stream, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-    _current = lambda: stream(device())  # noqa: E731
-    return _current()
+    stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if stream and device:
+        return lambda: stream(device())
+    return lambda: torch.cuda.current_stream().cuda_stream
+
+
+_current = None
 
 
 def _s(stream):
+    global _current
     if stream is None:
+        if _current is None:
+            _current = _stream_source()
         return _current()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
