@@ -316,8 +316,7 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
         }
       }
       mma_commit(&bars.done);
-      bool d2 = false;
-      wait_bar(&bars.done, 0, d2);
+      mbar_drain(&bars.done, 0);
     }
     __syncwarp();
   } else if (warp == 5) {
@@ -351,8 +350,7 @@ __global__ void __launch_bounds__(32 * TA<HP, DH>::NWARPS, 1) tree_attn_kernel(c
         }
       }
       mma_commit(&bars.done);
-      bool d2 = false;
-      wait_bar(&bars.done, 0, d2);
+      mbar_drain(&bars.done, 0);
     }
     __syncwarp();
   } else if (warp == C::NWARPS - 1) {

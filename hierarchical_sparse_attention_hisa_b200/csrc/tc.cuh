@@ -76,6 +76,15 @@ HSA_DEV bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, int* err) {
   return mbar_wait_bounded(bar, parity, err, kWaitCycles);
 }
 
+// Waits for copies or MMAs that are on their way, before the CTA may exit. They
+// complete by themselves, so no error flag cuts this wait short (other waits that
+// have given up must not let a CTA leave its shared memory and TMEM to the next
+// one early); it is bounded all the same, to about two milliseconds.
+HSA_DEV void mbar_drain(uint64_t* bar, uint32_t parity) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity) && clock64() - t0 < (1ll << 22)) {}
+}
+
 // Named barrier `id` over `count` threads (a multiple of 32) that also ORs a
 // predicate across them: every participant gets the same answer.
 HSA_DEV bool bar_or(int id, int count, bool v) {

@@ -266,6 +266,8 @@ __device__ void cached_block_scores(const TreeArgs& a, int64_t b, int tile, uint
       for (int i = 0; i < NH; ++i)
         if (n0 + i < a.T) out[int64_t(n0 + i) * a.ldb] = score_key(v[i]);
     }
+  } else if (tid == 0) {
+    mbar_drain(bar, 0);
   }
   tc_fence_before();
   __syncthreads();
@@ -383,9 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_token_scores_kernel(const __
         }
         ++it;
       }
-      bool d2 = false;  // drain armed loads before the CTA may exit
       for (uint32_t u = (it >= uint32_t(C::NS) ? it - C::NS : 0); u < it; ++u)
-        tw_wait(&full[u % C::NS], (u / C::NS) & 1, d2);
+        mbar_drain(&full[u % C::NS], (u / C::NS) & 1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -411,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_token_scores_kernel(const __
         ++it;
       }
       mma_commit(&done);
-      bool d2 = false;
-      tw_wait(&done, 0, d2);
+      mbar_drain(&done, 0);
     }
     __syncwarp();
   } else {
