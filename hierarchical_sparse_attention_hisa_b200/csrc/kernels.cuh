@@ -61,6 +61,8 @@ void launch_topm_from_keys(RowMap rm, int64_t rows, const uint32_t* bkeys, int64
 void launch_pair_lists(RowMap rm, int64_t rows, const int32_t* blocks, int B, int m, int k, int nbins,
                        int* cnt, int* off, int* cursor, int4* tiles, int* ntiles, uint32_t* pairs,
                        cudaStream_t s);
+// Whether launch_topk_from_keys has a CTA with the whole row in shared memory for these sizes.
+bool topk_rows_takes(int B, int m);
 void launch_topk_from_keys(RowMap rm, int64_t rows, const int32_t* blocks, const uint32_t* tkeys, int B,
                            int m, int k, int32_t* indices, cudaStream_t s, bool pdl = false);
 // (also appends each sequence's new token: k_idx/K/V rows and a completed block's sum)
@@ -110,9 +112,18 @@ struct TreeArgs {
 };
 constexpr int kTreeAttnCtas = 148;  // one per SM
 constexpr int kBkeys0 = 3;          // so that block 1's key, the first candidate, is on 16 bytes
-// Rows up to which the wide top-k is taken: one wave of two CTAs per SM. Against the prefill's kernel and the
-// mapping launch, a whole step of 8 rows 34.8 and 42.7 us, of 512 rows 143.5 and 142.3, of 1024 rows 200 and 194.
-constexpr int kWideRows = 296;
+// A tree's top-k (launch_tree_topk: a wide CTA per row, which writes cache rows itself) against the prefill's
+// selection and a mapping launch. The prefill's CTA of 256 threads with the row in shared memory, where it takes
+// the row at all (topk_rows_takes), is the faster one with more than 1024 candidates and more rows than the wide
+// CTAs, two to an SM, take in one wave. A whole step (us, wide / prefill's):
+//   m * B          288 rows    320       512       1024      8192
+//   1024           53 / 62*    65 / 74   75 / 84   107 / 118 593 / 659   (* 256 rows)
+//   4096           102 / 109   119 / 123 157 / 162 270 / 264 1796 / 1741
+//   8192           109 / 114   134 / 132 178 / 175 299 / 283 1960 / 1854
+// Rows that it does not take go to selections for a few rows of any length or a warp per row, always slower here:
+//   8000 (B = 100) 111 / 121*  131 / 226 172 / 267 302 / 380 2098 / 2319
+//   16384          123 / 150   143 / 280 195 / 329 342 / 445 2376 / 2804
+constexpr int kWideRows = 296, kWideKeys = 1024;
 // Token candidates of a query at position t: all up to it, or those of its m kept blocks.
 HSA_DEV int candidates(int t, int B, int m) { return t / B < m ? t + 1 : (m - 1) * B + t % B + 1; }
 void launch_tree_plan(int batch, int T, int64_t capacity, const int32_t* ctx, const int32_t* n_nodes,

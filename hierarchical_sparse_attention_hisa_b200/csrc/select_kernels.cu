@@ -983,12 +983,15 @@ void launch_pair_lists(RowMap rm, int64_t rows, const int32_t* blocks, int B, in
                 static_cast<const int*>(off), cursor, pairs, tiles);
 }
 
+bool topk_rows_takes(int B, int m) {
+  return int64_t(m) * B <= kRowCap && (B & (B - 1)) == 0 && B >= 4 && m <= 256;
+}
+
 void launch_topk_from_keys(RowMap rm, int64_t rows, const int32_t* blocks, const uint32_t* tkeys, int B,
                            int m, int k, int32_t* indices, cudaStream_t s, bool pdl) {
   if (rows == 0) return;
   count_launches(1);
-  if (int64_t(m) * B <= kRowCap && (B & (B - 1)) == 0 && B >= 4 && m <= 256 &&
-      (reinterpret_cast<uintptr_t>(tkeys) & 15u) == 0) {
+  if (topk_rows_takes(B, m) && (reinterpret_cast<uintptr_t>(tkeys) & 15u) == 0) {
     // rows of up to 8192 candidates: a 256-thread CTA per row, the row staged in shared memory
     cudaFuncSetAttribute(topk_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(RowSmem)));
     launch_kernel(pdl, topk_rows_kernel, unsigned(rows), kRowNT, sizeof(RowSmem), s, rm, blocks, tkeys, B, m, k,

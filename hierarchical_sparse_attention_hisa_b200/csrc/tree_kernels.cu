@@ -783,7 +783,10 @@ void launch_tree_topm(const TreeArgs& a, int64_t rows, int32_t* blocks, cudaStre
   else go(tree_topm_kernel<1024, 16>, 1024);  // (at most 16384 blocks)
 }
 
-bool tree_topk_wide(const TreeArgs& a, int64_t rows) { return rows <= kWideRows && int64_t(a.m) * a.B <= 16384; }
+bool tree_topk_wide(const TreeArgs& a, int64_t rows) {
+  const int64_t n = int64_t(a.m) * a.B;
+  return n <= 16384 && (rows <= kWideRows || n <= kWideKeys || !topk_rows_takes(a.B, a.m));
+}
 
 void launch_tree_topk(const TreeArgs& a, int64_t rows, int32_t* idx, cudaStream_t s) {
   const int64_t n = int64_t(a.m) * a.B;
@@ -805,7 +808,9 @@ void launch_tree_combine(const TreeArgs& a, int64_t rows, const void* Q, const i
                          const float* Opart, const float* mpart, const float* lpart, cudaStream_t s) {
   const dim3 grid{unsigned(kTreeAttnCtas), unsigned((a.H * a.d + 1023) / 1024)};
   count_launches(1);
-  // few rows are cut into many parts, many rows into two: there fewer registers put the grid into one wave
+  // few rows are cut into many parts, many rows into two: there fewer registers put the grid into one wave. A
+  // whole step (us, 16 parts at a time / 4): 1 row 36.9 / 38.9, 16 rows 41.9 / 43.0, 24 rows 49.1 / 49.2, 32 rows
+  // 49.2 / 47.1 (of k = 512 and H = 8: 41.0 / 43.0), 64 rows 63.5 / 61.4, 256 rows 108.6 / 106.5 (k = 2048, H = 64)
   auto kern = rows <= 32 ? (a.d == 128 ? tree_combine_kernel<128, 16> : tree_combine_kernel<64, 16>)
                          : (a.d == 128 ? tree_combine_kernel<128, 4> : tree_combine_kernel<64, 4>);
   launch_kernel(true, kern, grid, 256, 0, s, a, (const uint16_t*)Q, idx, scale, Opart, mpart, lpart);
