@@ -318,6 +318,10 @@ HSA_API int hsa_tree_workspace_size(const hsa_params* p, int32_t batch, int32_t 
  * of each node, ascending, -1 padded (an entry below ctx_len is that position,
  * entry ctx_len + j is drafted node j). A node that takes no part writes
  * nothing to the caches; its O row is zero and its indices are -1.
+ * The same call gives the same bits again. With other sequences beside it a
+ * node's O may differ in its last bits, and near-ties of real-valued scores may
+ * fall the other way: the attention's tiles are shared out over the whole batch,
+ * and the kernels for scores and selection go by the number of nodes in it.
  * batch * capacity, batch * T * m, batch * T * H and batch * T * 64 must stay
  * below 2^31, and capacity / B is at most 16384 blocks. Calls that may overlap on the GPU
  * (other streams, several captured graphs) need workspaces of their own. */
@@ -335,7 +339,7 @@ HSA_API int hsa_tree_step(const hsa_params* p, int32_t batch, int32_t T, int64_t
  * length.
  *   accepted [batch] int32: the last accepted node, or -1 for none. A sequence
  *   whose entry is no node of the plan is left as it is.
- * Of p, B, d_idx and d are used. One launch. */
+ * p is checked as by hsa_tree_step; B, d_idx and d are used. One launch. */
 HSA_API int hsa_tree_commit(const hsa_params* p, int32_t batch, int32_t T, int64_t capacity,
                             int32_t* ctx_len, const int32_t* paths, const int32_t* accepted,
                             hsa_bf16* k_idx_cache, hsa_bf16* K_cache, hsa_bf16* V_cache,
@@ -365,10 +369,10 @@ HSA_API int hsa_device_status(int reset);
  * bounded wait of the tensor-core kernels (block/token/tree scoring, attention)
  * gives up after about a millisecond instead of about two seconds, and the
  * next launch of each of them loses one producer hand-off in its first CTA
- * (the scoring kernels skip producing their first tile; the attention's first
- * K-tile arrival is not made), so a consumer's wait must run out. The kernels
- * then return with incomplete outputs and hsa_device_status reports
- * HSA_ERR_TIMEOUT. Nothing faults, traps or spins without bound. With on == 0
+ * (the scoring kernels skip producing their first tile, but for the tree's
+ * block scoring, which has no producer; the attention's first K-tile arrival is
+ * not made), so a consumer's wait must run out. The kernels then return with
+ * incomplete outputs and hsa_device_status reports HSA_ERR_TIMEOUT. Nothing faults, traps or spins without bound. With on == 0
  * the kernels behave normally again; clear the flag with
  * hsa_device_status(1) afterwards. Synchronous (cudaMemcpyToSymbol); returns
  * HSA_OK, or HSA_ERR_CUDA / HSA_ERR_DEVICE. */
