@@ -706,7 +706,10 @@ __global__ void __launch_bounds__(32 * Cfg<HP, DH>::NWARPS, 1) sparse_attn_tc_ke
         if (orow) {
 #pragma unroll
           for (int h = 0; h < HH; ++h) {
-            if (h0 + h < nh && r < DH) orow[(h0 + h) * DH + r] = cvt_bf16(ov[h] * linv[h0 + h]);
+            // (in the conversion's upper half: the single one, cvt_bf16, and the lower half each move the
+            // schedule around them by 0.3 % of the 64K prefill, 9.40 to 9.43 ms)
+            if (h0 + h < nh && r < DH)
+              orow[(h0 + h) * DH + r] = uint16_t(cvt_bf16x2(0.f, ov[h] * linv[h0 + h]) >> 16);
           }
         } else {
           // one part of a split query: unnormalised O^T, running maximum, row sum
